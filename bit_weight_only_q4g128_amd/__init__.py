@@ -17,6 +17,8 @@ __all__ = [
     "q4g128_gemv", "q4g128_gemv_grouped", "q4g128_gemv_grouped_noalloc", "NOALLOC_SCRATCH_BYTES", "nvfp4g16_gemv", "bf16_gemv", "q4g128_dequant_f32", "nvfp4g16_dequant_f32",
     "nvfp4g16_gemv_grouped", "nvfp4g16_workspace_bytes", "bf16_gemv_grouped", "bf16_workspace_bytes",
     "q4g128_gemv_fused", "q4g128_fused_workspace_bytes", "sample_topk", "bf16_head_sample", "bf16_head_sample_workspace_bytes", "q4g128_gemm", "gemv_grouped_mixed", "mixed_workspace_bytes",
+    "fp8b128_quantize", "fp8b128_gemm", "fp8b128_gemm_grouped", "fp8b128_workspace_bytes",
+    "verify_topk", "verify_topk_workspace_bytes", "verify_full", "verify_full_workspace_bytes",
     "variant_name", "strerror", "Q4GemvError", "LIB_PATH", "lib", "stream_read", "stream_read_sink_words",
     "VARIANT_AUTO", "VARIANT_DOT2", "VARIANT_MFMA", "VARIANT_STREAM", "VARIANT_TILED", "VARIANT_GEMM", "FMT_Q4G128", "FMT_NVFP4G16", "FMT_BF16",
 ]
@@ -119,6 +121,31 @@ lib.bf16_head_sample_ws.argtypes = [_p, _i, _i, _p, _i, _p, _f, _i, _p, _p, _p, 
 lib.bf16_head_sample_ws.restype = ctypes.c_int
 lib.bf16_head_sample_workspace_bytes.argtypes = [_i, _i, _i, _i]
 lib.bf16_head_sample_workspace_bytes.restype = ctypes.c_size_t
+
+
+
+
+class Fp8Task(ctypes.Structure):
+    """Mirror of the C struct fp8b128_task."""
+    _fields_ = [("x", _p), ("xscale", _p), ("w", _p), ("wscale", _p), ("residual", _p), ("y", _p), ("N", _i), ("K", _i)]
+
+
+lib.fp8b128_quantize.argtypes = [_p, _p, _i, _i, _p, _p, _p]
+lib.fp8b128_quantize.restype = ctypes.c_int
+lib.fp8b128_gemm.argtypes = [_p, _p, _i, _i, _p, _p, _i, _p, _p, _p]
+lib.fp8b128_gemm.restype = ctypes.c_int
+lib.fp8b128_gemm_grouped_ws.argtypes = [ctypes.POINTER(Fp8Task), _i, _i, _p, ctypes.c_size_t, _p]
+lib.fp8b128_gemm_grouped_ws.restype = ctypes.c_int
+lib.fp8b128_workspace_bytes.argtypes = [ctypes.POINTER(Fp8Task), _i, _i, ctypes.POINTER(ctypes.c_size_t)]
+lib.fp8b128_workspace_bytes.restype = ctypes.c_int
+lib.q4_verify_topk.argtypes = [_p, _i, _i, _i, _p, _p, _p, _i, _p, _p, _f, _i, _p, _p, _p, _p, ctypes.c_size_t, _p]
+lib.q4_verify_topk.restype = ctypes.c_int
+lib.q4_verify_topk_workspace_bytes.argtypes = [_i, _i, _i, _i]
+lib.q4_verify_topk_workspace_bytes.restype = ctypes.c_size_t
+lib.q4_verify_full.argtypes = [_p, _i, _i, _i, _p, _p, _p, _p, _f, _p, _p, _p, _p, ctypes.c_size_t, _p]
+lib.q4_verify_full.restype = ctypes.c_int
+lib.q4_verify_full_workspace_bytes.argtypes = [_i, _i, _i]
+lib.q4_verify_full_workspace_bytes.restype = ctypes.c_size_t
 
 
 class Q4GemvError(ValueError):
@@ -598,3 +625,189 @@ def mixed_workspace_bytes(items) -> int:
     n = ctypes.c_size_t(0)
     _raise(lib.q4gemv_mixed_workspace_bytes(arr, len(items), M, ctypes.byref(n)))
     return int(n.value)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit block-scaled products and the verification of drafted tokens.  These
+# calls may be made while another device than the tensors' is current.
+# ---------------------------------------------------------------------------
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_BLOCK = 128
+
+
+def _tensor(t, name: str, dtypes, shape, device):
+    """A contiguous GPU tensor of this shape on this device, or an error that
+    names what is wrong."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, name: str, dtypes, ndim: int):
+    _check(t, name, dtypes, ndim)
+    return t.shape, t.device, t.data_ptr()
+
+
+def _optional(t, name: str, dtypes, shape, device):
+    return None if t is None else _tensor(t, name, dtypes, shape, device)
+
+
+def _scratch(workspace, device):
+    if workspace is None:
+        return None, 0
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _enqueue(fn, args, device):
+    """fn(*args, stream) on the device's current stream, with that device
+    current (a launch goes to the current device)."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise Q4GemvError(rc)
+
+
+def fp8b128_quantize(x, up=None, codes=None, scale=None):
+    """e4m3 codes [M, K] (torch.float8_e4m3fn) and fp32 scales
+    [M, ceil(K / 128)] of bf16 activations x, or of silu(x) * up; K a multiple
+    of 16.  codes and scale: outputs to write into.  Returns (codes, scale)."""
+    shape, device, xp = _first(x, "x", _U16, 2)
+    M, K = shape
+    upp = _optional(up, "up", _U16, shape, device)
+    G = (K + _BLOCK - 1) // _BLOCK
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device)
+    if scale is None:
+        scale = torch.empty((M, G), dtype=torch.float32, device=device)
+    cp = _tensor(codes, "codes", _E4M3, shape, device)
+    sp = _tensor(scale, "scale", _F32, (M, G), device)
+    _enqueue(lib.fp8b128_quantize, (xp, upp, M, K, cp, sp), device)
+    return codes, scale
+
+
+def _fp8_task_array(items):
+    items = list(items)
+    if not 1 <= len(items) <= 8:
+        raise ValueError("1..8 tasks per call")
+    arr = (Fp8Task * len(items))()
+    outs, M, device = [], None, None
+    for i, (x, x_scale, w, w_scale, residual, out) in enumerate(items):
+        (m, K), dev, xp = _first(x, f"task {i}: x", _E4M3, 2)
+        if M is None:
+            M, device = m, dev
+        elif m != M or dev != device:
+            raise ValueError("all tasks must share the batch size M and the device")
+        if not isinstance(w, torch.Tensor) or w.dim() != 2:
+            raise ValueError(f"task {i}: w must be a tensor of 2 dims")
+        N, G = w.shape[0], (K + _BLOCK - 1) // _BLOCK
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if out is None else out
+        outs.append(y)
+        arr[i] = Fp8Task(xp, _tensor(x_scale, "x_scale", _F32, (M, G), device), _tensor(w, "w", _E4M3, (N, K), device),
+                         _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), device),
+                         _optional(residual, "residual", _U16, (M, N), device),
+                         _tensor(y, "out", (torch.bfloat16,), (M, N), device), N, K)
+    return arr, len(items), outs, M, device
+
+
+def fp8b128_gemm_grouped(items, workspace=None):
+    """Several independent 8-bit block-scaled products with one batch size,
+    launched together.  items: sequence of (x, x_scale, w, w_scale,
+    residual-or-None, out-or-None): x e4m3 [M, K] with x_scale fp32
+    [M, ceil(K / 128)] (fp8b128_quantize makes both), w e4m3 [N, K] with
+    w_scale fp32 [ceil(N / 128), ceil(K / 128)], residual and out bf16 [M, N]
+    (out may be the residual).  workspace: optional uint8 device tensor of at
+    least fp8b128_workspace_bytes(items) bytes, zero-filled before its first
+    use and reusable afterwards without clearing (lets few rows split K).
+    Returns the list of outputs."""
+    arr, count, outs, M, device = _fp8_task_array(items)
+    wp, wn = _scratch(workspace, device)
+    _enqueue(lib.fp8b128_gemm_grouped_ws, (arr, count, M, wp, wn), device)
+    return outs
+
+
+def fp8b128_workspace_bytes(items) -> int:
+    arr, count, _, M, _ = _fp8_task_array(items)
+    n = ctypes.c_size_t(0)
+    _raise(lib.fp8b128_workspace_bytes(arr, count, M, ctypes.byref(n)))
+    return int(n.value)
+
+
+def fp8b128_gemm(x, x_scale, w, w_scale, residual=None, out=None, workspace=None):
+    """y[M, N] = sum over blocks of 128 columns of x_scale * w_scale * (x . W^T)
+    (+ residual), bf16: one product of fp8b128_gemm_grouped."""
+    return fp8b128_gemm_grouped([(x, x_scale, w, w_scale, residual, out)], workspace)[0]
+
+
+def verify_topk_workspace_bytes(B: int, D: int, V: int, top_k: int = 30) -> int:
+    """Bytes of workspace verify_topk uses (0: none)."""
+    return int(lib.q4_verify_topk_workspace_bytes(B, D, V, top_k))
+
+
+def verify_full_workspace_bytes(B: int, D: int, V: int) -> int:
+    """Bytes of workspace verify_full uses."""
+    return int(lib.q4_verify_full_workspace_bytes(B, D, V))
+
+
+def _verify_outputs(logits, draft, u, n_draft, need, workspace):
+    (B, D1, V), device, lp = _first(logits, "logits", _U16, 3)
+    D = D1 - 1
+    dp = _tensor(draft, "draft", _I32, (B, D), device)
+    up = _tensor(u, "u", _F32, (B, D1), device)
+    np_ = _optional(n_draft, "n_draft", _I32, (B,), device)
+    if workspace is None:
+        workspace = torch.empty(need(B, D, V), dtype=torch.uint8, device=device)
+    wp, wn = _scratch(workspace, device)
+    token = torch.empty((B, D1), dtype=torch.int32, device=device)
+    count = torch.empty((B,), dtype=torch.int32, device=device)
+    prob = torch.empty((B, D), dtype=torch.float32, device=device)
+    return B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob
+
+
+def verify_topk(logits, draft, u, draft_index=None, draft_prob=None, n_draft=None, temperature: float = 0.8, top_k: int = 30,
+                workspace=None):
+    """Verifies drafted tokens against the target's top-k distributions
+    (q4_verify_topk in the C header): logits bf16 [B, D + 1, V], draft int32
+    [B, D], u fp32 [B, D + 1] in [0, 1) (D acceptance uniforms, then the
+    draw's), the draft's distributions as draft_index int32 and draft_prob fp32
+    [B, D, k'] (sample_topk's outputs) or None for a draft certain of its
+    tokens, n_draft int32 [B] or None.  Returns (token int32 [B, D + 1]: the
+    tokens that stand, the one drawn after them, then -1; count int32 [B]: how
+    many stand; accept_prob fp32 [B, D])."""
+    B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob = _verify_outputs(
+        logits, draft, u, n_draft, lambda b, d, v: verify_topk_workspace_bytes(b, d, v, top_k), workspace)
+    kd = 0
+    if draft_index is not None:
+        if not isinstance(draft_index, torch.Tensor) or draft_index.dim() != 3:
+            raise ValueError("draft_index must be a tensor of 3 dims")
+        kd = draft_index.shape[2]
+    ip = _optional(draft_index, "draft_index", _I32, (B, D, kd), device)
+    pp = _optional(draft_prob, "draft_prob", _F32, (B, D, kd), device)
+    _enqueue(lib.q4_verify_topk, (lp, B, D, V, dp, ip, pp, kd, np_, up, temperature, top_k, token.data_ptr(), count.data_ptr(),
+                                  prob.data_ptr(), wp, wn), device)
+    return token, count, prob
+
+
+def verify_full(logits, draft, u, draft_logits=None, n_draft=None, temperature: float = 0.8, workspace=None):
+    """Verifies drafted tokens against the softmax of whole rows
+    (q4_verify_full in the C header): as verify_topk, with the draft's
+    distributions as draft_logits bf16 [B, D, V] or None."""
+    B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob = _verify_outputs(logits, draft, u, n_draft,
+                                                                                   verify_full_workspace_bytes, workspace)
+    qp = _optional(draft_logits, "draft_logits", _U16, (B, D, V), device)
+    _enqueue(lib.q4_verify_full, (lp, B, D, V, dp, qp, np_, up, temperature, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
+                                  wp, wn), device)
+    return token, count, prob

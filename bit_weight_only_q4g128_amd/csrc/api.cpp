@@ -4,10 +4,15 @@
 #include <stdint.h>
 
 #include "q4gemv.h"
+#include "api_util.h"
 #include "internal.h"
 
+using q4::aligned;
 using q4::Fmt;
 using q4::GemvArgs;
+using q4::overlaps;
+using q4::Range;
+using q4::range_of;
 
 namespace {
 
@@ -15,19 +20,6 @@ constexpr int kMaxM = 64;
 static_assert(Q4GEMV_NOALLOC_SCRATCH_BYTES == q4::kNoAllocScratchBytes, "header and library disagree on the built-in scratch");
 constexpr long kMaxK = 32768;
 constexpr long kMaxN = 1L << 24;
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + bytes};
-}
-
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 int check_common(const void* x, int M, int K, int N, const void* y) {
     if (!x || !y) return Q4_EINVAL_PTR;
@@ -892,11 +884,11 @@ const char* q4gemv_strerror(int status) {
         case Q4_EALIAS: return "output overlaps an input";
         case Q4_ELAUNCH: return "kernel launch failed";
         case Q4_EVARIANT: return "unknown variant or variant cannot run this shape";
-        case Q4_ESCRATCH: return "the call needs more split-K scratch than the built-in array holds";
+        case Q4_ESCRATCH: return "the call needs more scratch than the built-in array, or the given workspace, holds";
         default: return "unknown status";
     }
 }
 
-int q4gemv_version(void) { return 110; }
+int q4gemv_version(void) { return 120; }
 
 }  // extern "C"

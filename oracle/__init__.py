@@ -17,7 +17,9 @@ What it computes, in plain NumPy:
   * the fused neighbours of the product: RN_bf16 from fp64, the SiLU-gated
     activation h = RN_bf16(silu(g) * u), and the product plus a residual;
   * sampling from the head: top-k, softmax at a temperature, inverse-CDF draw
-    with a caller-supplied uniform.
+    with a caller-supplied uniform;
+  * the draft-and-verify operators (step.py): 8-bit block-scaled quantisation
+    and products, verification of drafted tokens from given uniforms.
 
 Every function is pinned by tests against values fixed outside this module
 (hand-worked examples, closed forms, exhaustive comparison with numpy/torch
@@ -43,4 +45,11 @@ from .reference import (  # noqa: F401
     sample_topk,
     GROUP_Q4,
     GROUP_NVFP4,
+)
+from .step import (  # noqa: F401
+    e4m3_nearest,
+    fp8_quantize,
+    fp8_gemm,
+    verify_topk,
+    verify_full,
 )

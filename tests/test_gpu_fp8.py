@@ -1,0 +1,419 @@
+"""GPU parity of the 8-bit block-scaled operators (fp8b128_quantize,
+fp8b128_gemm, fp8b128_gemm_grouped) against the fp64 oracle, through the
+binding.
+
+Tolerances.  Codes of plain activations and their scales are exact (one
+rounding each of a quantity that fp32 holds well enough).  Gated activations
+are fp32: exp2 and the quotient are each within 1 ulp (2^-23), the sum, the
+second exponential factor and the scale's own division round once (2^-24), so
+h is within 4 * 2^-23 and the scale within 5 * 2^-23 of its value; a code is
+within half an e4m3 step of the exact quotient plus 2^-20 of it (h, the block's
+largest and the two roundings of the quotient).
+
+Products.  The matrix cores add the products of 8 consecutive columns aligned
+to the largest of them and drop what lies below 2^-13 of it (measured, and held
+by test_octet_precision): each of the 7 others loses less than 2^-13 of the
+octet's largest product P, which is at most max|x| max|w| over the octet.
+Beyond that, with S[m, n] the sum of absolute values, every term meets at most
+128 additions inside a block, G + 8 outside (blocks, waves, slices) and three
+roundings of its scale and of the residual's sum, each within 2^-23 of the
+magnitude it meets (not 2^-24: truncation is allowed), and one rounding to
+bf16:
+    |y - y_ref| <= 7 * 2^-13 * sum_octets P + (128 + G + 16) * 2^-23 * S + 2^-8 |y_ref|.
+That is loose where much cancels, so every shape also runs on codes that are
+integers up to 15 with power-of-two scales: all products of an octet lie within
+13 bits of its largest, every sum is an integer below 2^24, nothing rounds
+before bf16 and the result has to be the exact one, bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from gpu_util import gpu, rn_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q4():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_weight_only_q4g128_amd as m
+    return m
+
+
+def activations(M, K, seed):
+    g = synth.make_gen(("fp8-x", M, K, seed))
+    loud = torch.where(torch.rand(K, generator=g) < 1 / 32, 10.0, 1.0)
+    return (torch.randn(M, K, generator=g) * loud).to(torch.bfloat16)
+
+
+def code_bytes(t):
+    return t.cpu().view(torch.uint8).numpy()
+
+
+# ---------------------------------------------------------------------------
+# quantisation
+# ---------------------------------------------------------------------------
+def check_plain(codes, scale, bits):
+    want, s = oracle.fp8_quantize(bits)
+    got = oracle.e4m3fn_value(code_bytes(codes))
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[~nan], want[~nan])
+    assert np.array_equal(scale.cpu().numpy(), s.astype(np.float32))
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 128), (1, 2048), (3, 144), (5, 2000), (7, 1008), (64, 8192), (257, 640), (2, 32768),
+                                 (1023, 112)])
+def test_quantize(q4, M, K):
+    print(f"quantize M={M} K={K}", flush=True)
+    x = activations(M, K, 0)
+    codes, scale = q4.fp8b128_quantize(gpu(x))
+    assert codes.dtype == torch.float8_e4m3fn and tuple(scale.shape) == (M, -(-K // 128))
+    check_plain(codes, scale, synth.bits16(x))
+
+
+def test_quantize_every_tie(q4):
+    """Blocks whose largest value is a power of two times 448, so that every
+    e4m3 code and every midpoint between codes is some value's quotient."""
+    v = oracle.e4m3fn_value(np.arange(0, 127, dtype=np.uint8))
+    mid = (v[:-1] + v[1:]) / 2
+    vals = np.concatenate([v, mid, -mid])
+    vals = vals[:: 1]
+    rows = []
+    for e in (-120, -30, 0, 30, 100):
+        part = np.full((-(-len(vals) // 127), 128), 448.0)
+        flat = part[:, 1:].reshape(-1)
+        flat[: len(vals)] = vals
+        part[:, 1:] = flat.reshape(part.shape[0], 127)
+        rows.append(np.ldexp(part, e))
+    x = torch.from_numpy(np.concatenate(rows)).to(torch.bfloat16)
+    codes, scale = q4.fp8b128_quantize(gpu(x))
+    check_plain(codes, scale, synth.bits16(x))
+
+
+def test_quantize_extremes(q4):
+    """Zero blocks, subnormal blocks, blocks near the largest bf16, values that
+    are not finite, signed zeros."""
+    x = activations(10, 256, 3)
+    x[0] = 0
+    x[1, :128] = -0.0
+    x[2] = x[2] * 2.0 ** -126
+    x[3] = x[3] * 2.0 ** -132
+    x[4] = x[4] * 2.0 ** 122
+    x[5, 3], x[5, 77], x[5, 200] = float("inf"), float("-inf"), float("nan")
+    x[6] = float("nan")
+    x[7, :128] = float("inf")
+    x[8, 1] = 3.3895e38
+    x[9] = 0
+    x[9, 255] = 1e-40
+    codes, scale = q4.fp8b128_quantize(gpu(x))
+    check_plain(codes, scale, synth.bits16(x))
+
+
+@pytest.mark.parametrize("M,K", [(1, 128), (3, 2000), (48, 8192), (240, 1040)])
+def test_quantize_gated(q4, M, K):
+    print(f"quantize gated M={M} K={K}", flush=True)
+    g, u = activations(M, K, 1), activations(M, K, 2)
+    codes, scale = q4.fp8b128_quantize(gpu(g), up=gpu(u))
+    gb, ub = synth.bits16(g), synth.bits16(u)
+    _, s = oracle.fp8_quantize(gb, ub)
+    assert np.all(np.abs(scale.cpu().numpy() - s) <= 5 * 2.0 ** -23 * s)
+    gv, uv = oracle.bf16_value(gb), oracle.bf16_value(ub)
+    t = gv / (1 + np.exp(-gv)) * uv / np.where(s > 0, s, 1.0).repeat(128, 1)[:, :K]
+    e = np.clip(np.frexp(np.abs(t))[1] - 1, -6, 8)
+    half = np.ldexp(0.5, e - 3)
+    got = oracle.e4m3fn_value(code_bytes(codes))
+    assert np.all(np.abs(got - t) <= half + 2.0 ** -20 * np.abs(t))
+
+
+def test_quantize_gated_extremes(q4):
+    """Far gates (silu underflows or is the identity), products past fp32, and
+    gates that are not finite."""
+    g, u = activations(6, 128, 5), activations(6, 128, 6)
+    g[0], g[1] = 200.0, -200.0
+    g[2, :4] = torch.tensor([1e30, -1e30, 3e38, -3e38], dtype=torch.bfloat16)
+    g[3, 5], u[3, 9] = float("inf"), float("nan")
+    g[4], u[4] = 1e30, 1e30
+    u[5] = 0
+    codes, scale = q4.fp8b128_quantize(gpu(g), up=gpu(u))
+    want, s = oracle.fp8_quantize(synth.bits16(g), synth.bits16(u))
+    got, sc = oracle.e4m3fn_value(code_bytes(codes)), scale.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    for r in (0, 2, 3, 5):
+        assert np.all(np.abs(sc[r] - s[r]) <= 5 * 2.0 ** -23 * s[r]), r
+    assert sc[1, 0] < 1e-30 and sc[4, 0] == 0
+
+
+def test_quantize_into_outputs(q4):
+    """Given outputs are written whole and nothing beside them."""
+    M, K = 5, 400
+    x = activations(M, K, 7)
+    buf = torch.full((M * K + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    sbuf = torch.full((M * 4 + 8,), -7.0, device="cuda")
+    codes, scale = buf[32:32 + M * K].view(M, K), sbuf[4:4 + M * 4].view(M, 4)
+    a, b = q4.fp8b128_quantize(gpu(x), codes=codes, scale=scale)
+    assert a is codes and b is scale
+    check_plain(codes, scale, synth.bits16(x))
+    assert bool((buf[:32] == 0x55).all() and (buf[32 + M * K:] == 0x55).all())
+    assert bool((sbuf[:4] == -7).all() and (sbuf[4 + M * 4:] == -7).all())
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+def operands(M, N, K, seed):
+    """Codes of quantised activations and weights, scales over a few binades."""
+    g = synth.make_gen(("fp8-gemm", M, N, K, seed))
+    G = -(-K // 128)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    w = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    xs = torch.exp(torch.randn(M, G, generator=g)) * 0.01
+    ws = torch.exp(torch.randn(-(-N // 128), G, generator=g)) * 0.001
+    return x, xs, w, ws
+
+
+def to_gpu(ops):
+    return tuple(t.cuda().contiguous() for t in ops)
+
+
+def octets(ops):
+    """Sum over octets of 8 columns of xs * ws * max|x| * max|w|."""
+    x, xs, w, ws = ops
+    top = lambda c: np.abs(oracle.e4m3fn_value(code_bytes(c))).reshape(c.shape[0], -1, 8).max(2)  # noqa: E731
+    K8 = x.shape[1] // 8
+    sx = xs.double().numpy().repeat(16, 1)[:, :K8]
+    sw = ws.double().numpy().repeat(16, 1)[:, :K8].repeat(128, 0)[:w.shape[0]]
+    return (top(x) * sx) @ (top(w) * sw).T
+
+
+def whole_operands(M, N, K, seed):
+    """Codes that are integers -15 .. 15, scales powers of two equal within a
+    row of blocks: every product sums exactly."""
+    g = synth.make_gen(("fp8-whole", M, N, K, seed))
+    G = -(-K // 128)
+    ints = lambda *s: torch.randint(-15, 16, s, generator=g).float().to(torch.float8_e4m3fn)  # noqa: E731
+    xs = torch.ldexp(torch.ones(M, G), torch.randint(-8, 8, (M, 1), generator=g))
+    ws = torch.ldexp(torch.ones(-(-N // 128), G), torch.randint(-8, 8, (-(-N // 128), 1), generator=g))
+    return ints(M, K), xs, ints(N, K), ws
+
+
+def check_whole(y, ops):
+    x, xs, w, ws = ops
+    ref = oracle.fp8_gemm(code_bytes(x), xs.numpy(), code_bytes(w), ws.numpy())
+    assert np.array_equal(y.cpu().view(torch.int16).numpy().view(np.uint16), rn_bf16_bits(ref))
+
+
+def check_gemm(y, ops, resid=None, what=""):
+    x, xs, w, ws = ops
+    xb, wb = code_bytes(x), code_bytes(w)
+    rb = None if resid is None else synth.bits16(resid)
+    ref = oracle.fp8_gemm(xb, xs.numpy(), wb, ws.numpy(), rb)
+    S = oracle.fp8_gemm(xb & 0x7F, np.abs(xs.numpy()), wb & 0x7F, np.abs(ws.numpy()))
+    if resid is not None:
+        S = S + np.abs(oracle.bf16_value(rb))
+    got = y.cpu().double().numpy()
+    G = xs.shape[1]
+    bound = 7 * 2.0 ** -13 * octets(ops) + (128 + G + 16) * 2.0 ** -23 * S + 2.0 ** -8 * np.abs(ref)
+    bad = ~(np.abs(got - ref) <= bound)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} outside; first at {i}: {got[i]} ref {ref[i]} bound {bound[i]}")
+
+
+# every row class of the batch, ragged weight rows, K from one chunk of a block
+# to many blocks, blocks that K ends inside
+SHAPES = [(1, 1, 16), (1, 17, 128), (1, 2048, 2048), (1, 2048, 8192), (1, 500, 4112), (2, 129, 144), (3, 64, 1040), (8, 300, 2000),
+          (15, 513, 256), (16, 1000, 640), (17, 65, 2048), (31, 2049, 512), (33, 130, 8192), (48, 2048, 2048), (48, 2048, 8192),
+          (49, 77, 384), (64, 4097, 256), (65, 640, 272), (100, 2049, 2048), (127, 129, 1920), (128, 128, 128), (129, 255, 400),
+          (240, 1025, 2048), (255, 257, 1152), (256, 512, 4096), (257, 513, 656), (300, 2049, 784), (513, 770, 1024),
+          (1000, 333, 2064), (1025, 1281, 272)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(q4, M, N, K):
+    print(f"gemm M={M} N={N} K={K}", flush=True)
+    ops = operands(M, N, K, 0)
+    d = to_gpu(ops)
+    y = q4.fp8b128_gemm(*d)
+    check_gemm(y, ops, what="plain")
+    whole = whole_operands(M, N, K, 0)
+    e = to_gpu(whole)
+    check_whole(q4.fp8b128_gemm(*e), whole)
+    items = [(*d, None, None)]
+    need = q4.fp8b128_workspace_bytes(items)
+    if need:
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        for rep in range(2):
+            z = q4.fp8b128_gemm(*d, workspace=ws)
+            check_gemm(z, ops, what=f"workspace call {rep}")
+            assert int(ws[:65536].count_nonzero()) == 0, "arrival counters not left at zero"
+            if rep:
+                assert torch.equal(z, first), "two calls differ"
+            first = z
+        check_whole(q4.fp8b128_gemm(*e, workspace=ws), whole)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 512), (4, 2048, 8192), (48, 130, 1040), (130, 257, 272), (300, 600, 512)])
+def test_gemm_residual(q4, M, N, K):
+    print(f"gemm residual M={M} N={N} K={K}", flush=True)
+    ops = operands(M, N, K, 1)
+    d = to_gpu(ops)
+    r = (torch.randn(M, N, generator=synth.make_gen(("fp8-r", M, N))) * 4).to(torch.bfloat16)
+    ws = torch.zeros(max(256, q4.fp8b128_workspace_bytes([(*d, gpu(r), None)])), dtype=torch.uint8, device="cuda")
+    for work in (None, ws):
+        rg = gpu(r)
+        y = q4.fp8b128_gemm(*d, residual=rg, workspace=work)
+        check_gemm(y, ops, r, "residual")
+        z = q4.fp8b128_gemm(*d, residual=rg, out=rg, workspace=work)       # in place
+        assert z is rg and torch.equal(z, y)
+
+
+def test_octet_precision(q4):
+    """Beside products P and -P, a product of 2^-13 P survives in P's octet of
+    columns, and one of 2^-24 P outside it."""
+    x, w = torch.zeros(6, 128), torch.zeros(6, 128)
+    want = []
+    for r, (i, j, k, e) in enumerate([(0, 1, 2, 3), (0, 64, 7, 3), (8, 3, 9, 3), (0, 1, 9, -8), (0, 127, 64, -7), (40, 41, 100, -8)]):
+        x[r, i] = x[r, j] = 256
+        w[r, i], w[r, j] = 256, -256
+        x[r, k], w[r, k] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+        want.append(2.0 ** e)
+    one = torch.ones(6, 1)
+    y = q4.fp8b128_gemm(*to_gpu((x.to(torch.float8_e4m3fn), one, w.to(torch.float8_e4m3fn), torch.ones(1, 1))))
+    assert torch.diagonal(y).float().cpu().tolist() == want
+
+
+@pytest.mark.parametrize("M", [1, 5, 20, 48, 100, 256])
+def test_gemm_one_hot_is_exact(q4, M):
+    """Activations with one nonzero code per row and power-of-two scales: every
+    sum has one term, so y is the weight times its scales, rounded once; each
+    batch row reads another column, so a column misplaced within a block or a
+    scale of another block would show."""
+    N, K = 260, 656
+    _, _, w, ws = operands(1, N, K, 2)
+    ks = np.random.default_rng(M).choice(K, size=M)
+    ks[0] = K - 1
+    x = torch.zeros(M, K)
+    x[torch.arange(M), torch.from_numpy(ks)] = 1.0
+    xs = torch.from_numpy(np.ldexp(1.0, np.random.default_rng(M + 1).integers(-6, 6, (M, 6))).astype(np.float32))
+    y = q4.fp8b128_gemm(*to_gpu((x.to(torch.float8_e4m3fn), xs, w, ws)))
+    wv = oracle.e4m3fn_value(code_bytes(w)).astype(np.float32)
+    rows = np.arange(N) // 128
+    want = (wv[:, ks] * ws.numpy()[rows][:, ks // 128]).T * xs.numpy()[np.arange(M), ks // 128][:, None]
+    # w * (xs * ws): xs is a power of two, so one fp32 rounding, then bf16's; the
+    # kernel's product of the scales and its fma round at the same places
+    assert np.array_equal(y.cpu().view(torch.int16).numpy().view(np.uint16), rn_bf16_bits(want))
+
+
+def test_gemm_unaligned_outputs(q4):
+    """Outputs and residuals on any even address, rows of odd length, rows
+    behind the last left as they were."""
+    for M, N, K in ((3, 131, 256), (70, 132, 256), (130, 260, 384)):
+        ops = operands(M, N, K, 4)
+        d = to_gpu(ops)
+        buf = torch.full((M * N + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = buf[1:1 + M * N].view(M, N)
+        r = gpu((torch.randn(M * N + 3, generator=synth.make_gen(("fp8-u", M))) * 4).to(torch.bfloat16))[3:].view(M, N)
+        q4.fp8b128_gemm(*d, residual=r, out=y)
+        check_gemm(y, ops, r.cpu(), f"{M} {N} {K}")
+        assert bool((buf[:1] == 7).all() and (buf[1 + M * N:] == 7).all())
+
+
+def test_gemm_nan_stays_in_its_row_and_column(q4):
+    for M, N, K in ((5, 140, 256), (140, 300, 256)):
+        x, xs, w, ws = operands(M, N, K, 5)
+        clean = q4.fp8b128_gemm(*to_gpu((x, xs, w, ws)))
+        xb, wb = x.view(torch.uint8).clone(), w.view(torch.uint8).clone()
+        xb[2, 5], wb[133, 200] = 0x7F, 0xFF
+        y = q4.fp8b128_gemm(*to_gpu((xb.view(torch.float8_e4m3fn), xs, wb.view(torch.float8_e4m3fn), ws)))
+        nan = torch.isnan(y)
+        want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+        want[2], want[:, 133] = True, True
+        assert torch.equal(nan, want)
+        assert torch.equal(y[~want], clean[~want])
+
+
+@pytest.mark.parametrize("M", [1, 16, 48, 100])
+def test_group_equals_single_calls(q4, M):
+    """Projections that read one input, and one of another K, in one call."""
+    tasks = [operands(M, N, 2048, 10 + i) for i, N in enumerate((2048, 512, 515, 1030))] + [operands(M, 300, 400, 20)]
+    tasks = [(tasks[0][0], tasks[0][1], *t[2:]) if t[0].shape[1] == 2048 else t for t in tasks]
+    d = [to_gpu(t) for t in tasks]
+    r = gpu((torch.randn(M, 515, generator=synth.make_gen(("fp8-g", M)))).to(torch.bfloat16))
+    items = [(*t, r if i == 2 else None, None) for i, t in enumerate(d)]
+    ws = torch.zeros(max(256, q4.fp8b128_workspace_bytes(items)), dtype=torch.uint8, device="cuda")
+    for work in (None, ws):
+        outs = q4.fp8b128_gemm_grouped(items, workspace=work)
+        for i, (y, t) in enumerate(zip(outs, tasks)):
+            check_gemm(y, t, r.cpu() if i == 2 else None, f"task {i}")
+
+
+def test_another_stream_and_graph(q4):
+    """Quantisation into products on a side stream, then the same captured and
+    replayed with other inputs in between."""
+    M, N, K = 20, 1030, 2048
+    _, _, w, ws = to_gpu(operands(1, N, K, 30))
+    xin = gpu(activations(M, K, 31))
+    work = torch.zeros(max(256, q4.fp8b128_workspace_bytes([(*to_gpu(operands(M, N, K, 30)), None, None)])), dtype=torch.uint8,
+                       device="cuda")
+
+    def step():
+        codes, scale = q4.fp8b128_quantize(xin)
+        return q4.fp8b128_gemm(codes, scale, w, ws, workspace=work)
+
+    eager = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(eager, other)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for rep in range(3):
+        xin.copy_(gpu(activations(M, K, 40 + rep)))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step()), f"replay {rep}"
+    del g
+
+
+def test_binding_refusals(q4):
+    x, xs, w, ws = to_gpu(operands(4, 256, 256, 50))
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x, xs[:, :1].contiguous(), w, ws)              # one scale column short
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x, xs, w, ws[:1].contiguous())                 # one block of rows short
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x.view(torch.uint8).t(), xs, w, ws)            # strided
+    with pytest.raises(TypeError):
+        q4.fp8b128_gemm(x.view(torch.int8), xs, w, ws)
+    with pytest.raises(TypeError):
+        q4.fp8b128_gemm(x, xs.double(), w, ws)
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x, xs, w.view(torch.uint8)[:, :128].contiguous(), ws)
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x, xs, w, ws, residual=torch.zeros(4, 255, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm(x, xs.cpu(), w, ws)
+    with pytest.raises(ValueError):
+        q4.fp8b128_gemm_grouped([])
+    with pytest.raises(q4.Q4GemvError) as e:
+        q4.fp8b128_quantize(torch.zeros(2, 24, dtype=torch.bfloat16, device="cuda"))
+    assert e.value.status == -2
+    with pytest.raises(ValueError):
+        q4.fp8b128_quantize(torch.zeros(2, 32, dtype=torch.bfloat16, device="cuda"),
+                            up=torch.zeros(2, 16, dtype=torch.bfloat16, device="cuda"))
+    y = torch.full((4, 256), 3.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(q4.Q4GemvError) as e:
+        q4.fp8b128_gemm_grouped([(x, xs, w, ws, None, y), (x, xs, w, ws, None, y)])     # one output twice
+    assert e.value.status == -4
+    torch.cuda.synchronize()
+    assert bool((y == 3).all()), "a refused call wrote its output"
