@@ -151,11 +151,155 @@ hipError_t launch_rows(const Fp8Args* tasks, int count, int M, hipStream_t s) {
     return launch_kernel(fp8_rows_kernel<MT, R>, dim3(p.first[count], (M + 16 * MT - 1) / (16 * MT)), dim3(kWaves * 64), 0, s, p);
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: workgroup tiles of BM batch rows x BN weight rows over all of K,
+// WM x WN waves, each BM / WM x BN / WN.  Per 128-column block the tile's rows
+// go straight from memory to LDS (16 bytes per lane, no registers), into one
+// of two stages: while the waves compute a block, the next one is on its way;
+// one barrier per block.
+//
+// LDS holds rows of 128 bytes; 16-byte chunk c of row r sits at chunk
+// c ^ (r % 8), so that the rows of one fragment read fall into different banks.
+// The swizzle is on the memory side of the load: LDS is written in lane order.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void lds_void;
+// read through the scalar cache (a vector load would join the queue of the
+// loads to LDS, and its wait would wait for all of them)
+typedef const __attribute__((address_space(4))) float const_float;
+
+template <int BM, int BN>
+struct TileLds {
+    static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4;
+};
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
+    using L = TileLds<BM, BN>;
+    constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int kXLoads = BM / 8 / kW, kWLoads = BN / 8 / kW;      // 1 KB loads per wave and block
+    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && BN / WN <= 128 && BM / 64 <= kW, "tile");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * L::kStage];
+
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    // the tile: XCD-contiguous ranges of one task's tiles, walked in
+    // super-rows of 8 batch blocks
+    int ti = 0;
+    while (ti + 1 < p.count && (int)blockIdx.x >= p.first[ti + 1]) ++ti;
+    const Fp8Args a = p.t[ti];
+    const int nM = (p.M + BM - 1) / BM, nN = (a.N + BN - 1) / BN;
+    const int T = nM * nN, i = (int)blockIdx.x - p.first[ti], xcd = i & 7, q8 = T >> 3, r8 = T & 7;
+    const int tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (i >> 3);
+    const int per_super = 8 * nN, sup = tile / per_super, within = tile - sup * per_super;
+    const int rows_here = nM - sup * 8 < 8 ? nM - sup * 8 : 8;
+    const int m0 = (sup * 8 + within % rows_here) * BM, n0 = within / rows_here * BN;
+
+    const int K = a.K, G = (K + 127) >> 7;
+    const int rows_m = p.M - m0 < BM ? p.M - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
+    const int nb = (n0 + wn * (BN / WN)) >> 7;
+    const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(nb * 128 < a.N ? nb : 0) * G);
+
+    // this lane's place in a 1 KB load: row lane / 8 of the 8, chunk lane % 8
+    // of LDS = chunk (lane % 8) ^ (row % 8) of memory
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
+    const uint32_t off = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)K + chunk;
+    const uint32_t soff = (uint32_t)(64 * wave + lane) * (uint32_t)G * 4u;
+    const bool tail = K & 127;
+    auto load = [&](int g) {
+        uint8_t* st = lds + (g & 1) * L::kStage;
+        // a column past K reads as zero, as do rows past the matrix
+        const uint32_t o = tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K ? 0xFFFF0000u : off;
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(st + L::kX + (wave + kW * j) * 1024), 16, (int)o,
+                                                     j * kW * 8 * K + g * 128, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + L::kW + (wave + kW * j) * 1024), 16, (int)o,
+                                                     j * kW * 8 * K + g * 128, 0, 0);
+        if (wave < BM / 64)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(st + L::kS + wave * 256), 4, (int)soff, g * 4, 0, 0);
+    };
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int u = 0; u < TM; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int c0 = ((2 * lq) ^ (lr & 7)) * 16, c1 = ((2 * lq + 1) ^ (lr & 7)) * 16;
+    const int xrow = L::kX + (wm * (BM / WM) + lr) * 128, wrow = L::kW + (wn * (BN / WN) + lr) * 128;
+    load(0);
+    float next = wsrow[0];
+    for (int g = 0; g < G; ++g) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+        __syncthreads();
+        const float s = next;
+        if (g + 1 < G) {
+            load(g + 1);
+            next = wsrow[g + 1];
+        }
+        const uint8_t* st = lds + (g & 1) * L::kStage;
+        u32x4 xf[TM][2];
+        float f[TM];
+#pragma unroll
+        for (int u = 0; u < TM; ++u) {
+            xf[u][0] = *reinterpret_cast<const u32x4*>(st + xrow + u * 2048 + c0);
+            xf[u][1] = *reinterpret_cast<const u32x4*>(st + xrow + u * 2048 + c1);
+            f[u] = *reinterpret_cast<const float*>(st + L::kS + (wm * (BM / WM) + 16 * u + lr) * 4) * s;
+        }
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            u32x4 wf[2];
+            wf[0] = *reinterpret_cast<const u32x4*>(st + wrow + t * 2048 + c0);
+            wf[1] = *reinterpret_cast<const u32x4*>(st + wrow + t * 2048 + c1);
+            f32x4 d[TM];
+#pragma unroll
+            for (int u = 0; u < TM; ++u) d[u] = mfma(wf, xf[u]);
+#pragma unroll
+            for (int u = 0; u < TM; ++u)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[t][u][v] = __builtin_fmaf(f[u], d[u][v], acc[t][u][v]);
+        }
+    }
+
+    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+        const int m = m0 + wm * (BM / WM) + 16 * u + lr;
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            const int n = n0 + wn * (BN / WN) + 16 * t + 4 * lq;
+            if (n < a.N) store4(acc[t][u], a.resid, a.y, a.N, m, n, vec, rvec);
+        }
+    }
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tile(const Fp8Args* tasks, int count, int M, hipStream_t s) {
+    Fp8Group p;
+    p.count = count;
+    p.M = M;
+    p.first[0] = 0;
+    for (int i = 0; i < count; ++i) {
+        p.t[i] = tasks[i];
+        p.first[i + 1] = p.first[i] + ((M + BM - 1) / BM) * ((tasks[i].N + BN - 1) / BN);
+    }
+    return launch_kernel(fp8_tile_kernel<BM, BN, WM, WN>, dim3(p.first[count]), dim3(64 * WM * WN), 0, s, p);
+}
+
 }  // namespace
 
 size_t fp8_gemm_ws_bytes(const Fp8Args*, int, int) { return 0; }
 
 hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void*, size_t, hipStream_t s) {
+    if (M > 128) return launch_tile<256, 256, 4, 2>(tasks, count, M, s);
     return M <= 16 ? launch_rows<1, 1>(tasks, count, M, s) : launch_rows<4, 1>(tasks, count, M, s);
 }
 
