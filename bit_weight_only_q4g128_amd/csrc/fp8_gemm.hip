@@ -159,26 +159,36 @@ hipError_t launch_rows(const Fp8Args* tasks, int count, int M, hipStream_t s) {
 // one barrier per block.
 //
 // LDS holds rows of 128 bytes; 16-byte chunk c of row r sits at chunk
-// c ^ (r % 8), so that the rows of one fragment read fall into different banks.
-// The swizzle is on the memory side of the load: LDS is written in lane order.
+// c ^ (r / 2 % 8), so that one chunk of 16 consecutive rows (a quarter of a
+// fragment read) covers the 64 banks once: 4 cycles per read, where chunk
+// c ^ (r % 8) takes 8.  The swizzle is on the memory side of the load: LDS is
+// written in lane order.
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void lds_void;
 // read through the scalar cache (a vector load would join the queue of the
 // loads to LDS, and its wait would wait for all of them)
 typedef const __attribute__((address_space(4))) float const_float;
 
+// Ends a phase of the tile kernel: nothing moves across, no wait is implied.
+__device__ __forceinline__ void phase() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int BM, int BN>
 struct TileLds {
-    static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4;
+    static constexpr int kXStage = BM * 128, kWStage = BN * 128;
+    static constexpr int kX = 0, kW = 2 * kXStage, kS = kW + 2 * kWStage;    // two stages of each
+    static constexpr int kQuad = BM * 16, kBytes = kS + 2 * kQuad;           // scales of 4 blocks per row, two such
 };
 
 template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
+__device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
     using L = TileLds<BM, BN>;
     constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kXLoads = BM / 8 / kW, kWLoads = BN / 8 / kW;      // 1 KB loads per wave and block
-    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && BN / WN <= 128 && BM / 64 <= kW, "tile");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * L::kStage];
+    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && BN / WN <= 128 && BM / 64 <= kW && kW % 2 == 0 && BM / 64 <= kW / 2, "tile");
 
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -191,8 +201,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
     const Fp8Args a = p.t[ti];
     const int nM = (p.M + BM - 1) / BM, nN = (a.N + BN - 1) / BN;
     const int T = nM * nN, i = (int)blockIdx.x - p.first[ti], xcd = i & 7, q8 = T >> 3, r8 = T & 7;
-    const int tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (i >> 3);
-    const int per_super = 8 * nN, sup = tile / per_super, within = tile - sup * per_super;
+    const int at_tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (i >> 3);
+    const int per_super = 8 * nN, sup = at_tile / per_super, within = at_tile - sup * per_super;
     const int rows_here = nM - sup * 8 < 8 ? nM - sup * 8 : 8;
     const int m0 = (sup * 8 + within % rows_here) * BM, n0 = within / rows_here * BN;
 
@@ -205,25 +215,38 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
     const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(nb * 128 < a.N ? nb : 0) * G);
 
     // this lane's place in a 1 KB load: row lane / 8 of the 8, chunk lane % 8
-    // of LDS = chunk (lane % 8) ^ (row % 8) of memory
-    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
+    // of LDS = chunk (lane % 8) ^ (row / 2 % 8) of memory (kW is even, so the
+    // wave's loads all lie in even or all in odd groups of 8 rows)
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 4) ^ ((wave & 1) << 2)) * 16u;
     const uint32_t off = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)K + chunk;
     const uint32_t soff = (uint32_t)(64 * wave + lane) * (uint32_t)G * 4u;
     const bool tail = K & 127;
+    constexpr int kLoads = kXLoads + kWLoads;
+    // Load j of block g.  o = at(g): this lane's offset, or one past the matrix
+    // for a column past K and for a block past the last; such loads, like rows
+    // past the matrix, put zeros into LDS.
+    auto at = [&](int g) { return g >= G || (tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K) ? 0xFFFF0000u : off; };
+    auto piece = [&](int g, uint32_t o, int j) {
+        const int i = j < kXLoads ? j : j - kXLoads;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(j < kXLoads ? rx : rw,
+                                                 (lds_void*)(lds + (j < kXLoads ? L::kX + (g & 1) * L::kXStage : L::kW + (g & 1) * L::kWStage) +
+                                                             (wave + kW * i) * 1024),
+                                                 16, (int)o, i * kW * 8 * K + g * 128, 0, 0);
+    };
+    // Scales of blocks 4 q .. 4 q + 3: a row's scales are adjacent, so four
+    // cost the lines of one (every block alone: 20 % of the whole kernel).  The
+    // last four end at G.
+    auto quad_first = [&](int q) { return 4 * q + 4 <= G ? 4 * q : G - 4; };
+    auto scales = [&](int g) {
+        if ((g & 3) || g >= G || wave >= BM / 64) return;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + L::kS + ((g >> 2) & 1) * L::kQuad + wave * 1024), 16, (int)soff,
+                                                 quad_first(g >> 2) * 4, 0, 0);
+    };
     auto load = [&](int g) {
-        uint8_t* st = lds + (g & 1) * L::kStage;
-        // a column past K reads as zero, as do rows past the matrix
-        const uint32_t o = tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K ? 0xFFFF0000u : off;
+        scales(g);
+        const uint32_t o = at(g);
 #pragma unroll
-        for (int j = 0; j < kXLoads; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(st + L::kX + (wave + kW * j) * 1024), 16, (int)o,
-                                                     j * kW * 8 * K + g * 128, 0, 0);
-#pragma unroll
-        for (int j = 0; j < kWLoads; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + L::kW + (wave + kW * j) * 1024), 16, (int)o,
-                                                     j * kW * 8 * K + g * 128, 0, 0);
-        if (wave < BM / 64)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(st + L::kS + wave * 256), 4, (int)soff, g * 4, 0, 0);
+        for (int j = 0; j < kLoads; ++j) piece(g, o, j);
     };
 
     f32x4 acc[TN][TM];
@@ -232,41 +255,86 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
 #pragma unroll
         for (int u = 0; u < TM; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int c0 = ((2 * lq) ^ (lr & 7)) * 16, c1 = ((2 * lq + 1) ^ (lr & 7)) * 16;
-    const int xrow = L::kX + (wm * (BM / WM) + lr) * 128, wrow = L::kW + (wn * (BN / WN) + lr) * 128;
-    load(0);
-    float next = wsrow[0];
-    for (int g = 0; g < G; ++g) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
-        __syncthreads();
-        const float s = next;
-        if (g + 1 < G) {
-            load(g + 1);
-            next = wsrow[g + 1];
-        }
-        const uint8_t* st = lds + (g & 1) * L::kStage;
-        u32x4 xf[TM][2];
+    const int c0 = ((2 * lq) ^ (lr >> 1)) * 16, c1 = ((2 * lq + 1) ^ (lr >> 1)) * 16;
+    uint32_t xat[2] = {(uint32_t)(L::kX + (wm * (BM / WM) + lr) * 128 + c0), (uint32_t)(L::kX + (wm * (BM / WM) + lr) * 128 + c1)};
+    uint32_t wat[2] = {(uint32_t)(L::kW + (wn * (BN / WN) + lr) * 128 + c0), (uint32_t)(L::kW + (wn * (BN / WN) + lr) * 128 + c1)};
+    // Two groups of waves take turns (one of each shares a SIMD): while one
+    // multiplies, the other reads its next fragments.  Phase 2 g: group 0 reads
+    // block g, group 1 multiplies block g - 1; phase 2 g + 1 the other way
+    // round.  Block g + 1 goes on its way in phase 2 g, when the last reads of
+    // its stage (block g - 1, group 1) are a barrier behind, and has arrived
+    // (every wave's vmcnt) by the barrier that ends phase 2 g + 1.
+    auto walk = [&](const bool kSecond) __attribute__((always_inline)) {
+        u32x4 xf[TM][2], wf[TN][2];
         float f[TM];
-#pragma unroll
-        for (int u = 0; u < TM; ++u) {
-            xf[u][0] = *reinterpret_cast<const u32x4*>(st + xrow + u * 2048 + c0);
-            xf[u][1] = *reinterpret_cast<const u32x4*>(st + xrow + u * 2048 + c1);
-            f[u] = *reinterpret_cast<const float*>(st + L::kS + (wm * (BM / WM) + 16 * u + lr) * 4) * s;
+        float next = wsrow[0];
+        load(0);
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+        phase();
+        if (kSecond) {
+            load(1);
+            phase();
         }
+        for (int g = 0; g < G; ++g) {
+            const float s = next;
+            if (g + 1 < G) next = wsrow[g + 1];
+            const uint8_t* sc = lds + L::kS + ((g >> 2) & 1) * L::kQuad + (g - quad_first(g >> 2)) * 4;
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            u32x4 wf[2];
-            wf[0] = *reinterpret_cast<const u32x4*>(st + wrow + t * 2048 + c0);
-            wf[1] = *reinterpret_cast<const u32x4*>(st + wrow + t * 2048 + c1);
-            f32x4 d[TM];
+            for (int u = 0; u < TM; ++u) {
 #pragma unroll
-            for (int u = 0; u < TM; ++u) d[u] = mfma(wf, xf[u]);
+                for (int h = 0; h < 2; ++h) xf[u][h] = *reinterpret_cast<const u32x4*>(lds + xat[h] + u * 2048);
+                f[u] = *reinterpret_cast<const float*>(sc + (wm * (BM / WM) + 16 * u + lr) * 16);
+            }
 #pragma unroll
-            for (int u = 0; u < TM; ++u)
+            for (int t = 0; t < TN; ++t)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[t][u][v] = __builtin_fmaf(f[u], d[u][v], acc[t][u][v]);
+                for (int h = 0; h < 2; ++h) wf[t][h] = *reinterpret_cast<const u32x4*>(lds + wat[h] + t * 2048);
+            // the other stage
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                xat[h] ^= L::kXStage;
+                wat[h] = L::kW + ((wat[h] - L::kW) ^ L::kWStage);
+            }
+            if (!kSecond) load(g + 1);
+            const uint32_t o = at(g + 2);
+#pragma unroll
+            for (int u = 0; u < TM; ++u) f[u] *= s;
+            if (kSecond) __builtin_amdgcn_s_waitcnt(0x0070);      // vmcnt(0), lgkmcnt(0)
+            else __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
+            phase();
+            __builtin_amdgcn_s_setprio(1);
+            // result i folds while the matrix cores work on i + 1 .. i + kAhead
+            constexpr int kAhead = 3, kN = TN * TM;
+            f32x4 d[kAhead + 1];
+#pragma unroll
+            for (int i = 0; i < kN + kAhead; ++i) {
+                if (i < kN) d[i % (kAhead + 1)] = mfma(wf[i / TM], xf[i % TM]);
+                if (i >= kAhead) {
+                    const int o = i - kAhead;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[o / TM][o % TM][v] = __builtin_fmaf(f[o % TM], d[o % (kAhead + 1)][v], acc[o / TM][o % TM][v]);
+                }
+                if (i < kN) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (i >= kAhead) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                if (kSecond && i < kN && i % (kN / kLoads) == 0) {
+                    piece(g + 2, o, i / (kN / kLoads));
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                }
+            }
+            // (the folds stay in this block: sunk into a later one they would cost the overlap)
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+                for (int u = 0; u < TM; ++u) asm volatile("" : "+v"(acc[t][u]));
+            __builtin_amdgcn_s_setprio(0);
+            if (!kSecond) __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0)
+            if (!kSecond || g + 1 < G) phase();
         }
-    }
+    };
+    if (wave < kW / 2) walk(false);
+    else walk(true);
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // no load to LDS outlives the workgroup
 
     const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
 #pragma unroll
@@ -279,6 +347,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
             if (n < a.N) store4(acc[t][u], a.resid, a.y, a.N, m, n, vec, rvec);
         }
     }
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[TileLds<BM, BN>::kBytes];
+    tile<BM, BN, WM, WN>(p, lds);
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -298,8 +372,15 @@ hipError_t launch_tile(const Fp8Args* tasks, int count, int M, hipStream_t s) {
 
 size_t fp8_gemm_ws_bytes(const Fp8Args*, int, int) { return 0; }
 
+// Fewest 128-column blocks of any task (the tile kernel needs kTileMinBlocks).
+static int min_blocks(const Fp8Args* tasks, int count) {
+    int g = tasks[0].K;
+    for (int i = 1; i < count; ++i) g = tasks[i].K < g ? tasks[i].K : g;
+    return (g + 127) / 128;
+}
+
 hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void*, size_t, hipStream_t s) {
-    if (M > 128) return launch_tile<256, 256, 4, 2>(tasks, count, M, s);
+    if (M > 128 && min_blocks(tasks, count) >= 4) return launch_tile<256, 256, 4, 2>(tasks, count, M, s);
     return M <= 16 ? launch_rows<1, 1>(tasks, count, M, s) : launch_rows<4, 1>(tasks, count, M, s);
 }
 
