@@ -18,16 +18,35 @@
 // lane l holds weight rows 4 (l / 16) + v, v = 0..3, of batch row l % 16.
 #include "fp8.h"
 #include "internal.h"
+#include "topk.h"
 
 namespace q4 {
 
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+// the weights' scales, through the scalar cache (a vector load would join the
+// queue of the loads to LDS, and its wait would wait for all of them)
+typedef const __attribute__((address_space(4))) float const_float;
 
 __device__ __forceinline__ u32x4 ld16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
+// Loads straight to LDS, 16 or 4 bytes per lane in lane order from LDS address
+// `to` on.  Assembly, because around the builtin the compiler waits for every
+// such load before any read of LDS, also of another stage; the kernels below
+// wait by themselves (vmcnt, then a barrier).  Nothing is written to registers.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uintptr_t>(base);
+    return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), (int)bytes, kBufferFlags};
+}
+__device__ __forceinline__ void to_lds16(i32x4 r, uint32_t off, uint32_t soff, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(r), "s"(soff), "s"(to));
+}
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
+
 __device__ __forceinline__ f32x4 mfma(const u32x4 (&a)[2], const u32x4 (&b)[2]) {
     const i32x8 av = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
     const i32x8 bv = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
@@ -62,29 +81,81 @@ __device__ __forceinline__ bool rows_aligned8(const uint16_t* p, int N) { return
 
 struct Fp8Group {
     Fp8Args t[kFp8MaxTasks];
-    int first[kFp8MaxTasks + 1];   // first row block of each task
+    int first[kFp8MaxTasks + 1];      // first workgroup of each task
+    int ks[kFp8MaxTasks];             // slices of K of each task
+    uint32_t tile0[kFp8MaxTasks];     // of the split tasks: first counter, and
+    size_t part0[kFp8MaxTasks];       // byte offset of the first partial tile
+    unsigned* cnt;
+    uint8_t* part;
     int count, M;
 };
 
-// A workgroup of eight waves owns 16 R weight rows and 16 MT batch rows; the
-// waves share the 128-column blocks of K and meet in LDS.
+// A workgroup's task, its tile within the task and its slice of K.
+struct Where {
+    int task, tile, slice;
+};
+__device__ __forceinline__ Where where(const Fp8Group& p, int block) {
+    int t = 0;
+    while (t + 1 < p.count && block >= p.first[t + 1]) ++t;
+    const int i = block - p.first[t], ks = p.ks[t];
+    return Where{t, i / ks, i % ks};
+}
+
+// Joins the slices of a tile: each of the first `waves` waves stores its NF
+// fragments; in the workgroup that arrives last they become the sums over the
+// slices, in slice order, and the result is true.
+constexpr int kCoherent = 16;    // buffer cache policy sc1: device-coherent, not held in the per-XCD L2
+template <int NF>
+__device__ __forceinline__ bool join(f32x4 (&v)[NF], const Fp8Group& p, const Where& at, int waves, int wave, int lane, unsigned* s_prev) {
+    const int ks = p.ks[at.task];
+    const uint32_t slice_bytes = (uint32_t)waves * NF * 1024u;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(p.part + p.part0[at.task] + (size_t)at.tile * ks * slice_bytes, (uint32_t)ks * slice_bytes);
+    const uint32_t mine = (uint32_t)(wave * NF * 64 + lane) * 16u;
+    if (wave < waves) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[i]), r, (int)(mine + i * 1024u),
+                                                   at.slice * (int)slice_bytes, kCoherent);
+    }
+    if (!arrive_last(p.cnt + (size_t)(p.tile0[at.task] + at.tile) * kCtrWords, ks, threadIdx.x, s_prev)) return false;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (wave >= waves) return true;
+    for (int s = 0; s < ks; ++s) {
+        u32x4 o[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            o[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(mine + i * 1024u), s * (int)slice_bytes, kCoherent));
+#pragma unroll
+        for (int i = 0; i < NF; ++i) v[i] += __builtin_bit_cast(f32x4, o[i]);
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup of eight waves owns 16 R weight rows and 16 MT batch
+// rows over a slice of K; the waves share the slice's blocks, each loading its
+// own fragments straight into registers, and meet in LDS.
+// ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 
 template <int MT, int R>
 __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
-    __shared__ __attribute__((aligned(16))) f32x4 part[kWaves][R * MT][64];
+    constexpr int kTiles = R * MT, kMine = (kTiles + kWaves - 1) / kWaves;
+    constexpr int U = R * MT <= 4 ? 4 : 2;     // blocks whose loads are in flight together
+    __shared__ __attribute__((aligned(16))) f32x4 part[kWaves][kTiles][64];
+    __shared__ unsigned s_prev;
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int ti = 0;
-    while (ti + 1 < p.count && (int)blockIdx.x >= p.first[ti + 1]) ++ti;
-    const Fp8Args a = p.t[ti];
-    const int n0 = ((int)blockIdx.x - p.first[ti]) * 16 * R, m0 = blockIdx.y * 16 * MT;
+    const Where at = where(p, blockIdx.x);
+    const Fp8Args a = p.t[at.task];
+    const int n0 = at.tile * 16 * R, m0 = blockIdx.y * 16 * MT;
     const int K = a.K, G = (K + 127) >> 7;
     const int rows_n = a.N - n0 < 16 * R ? a.N - n0 : 16 * R, rows_m = p.M - m0 < 16 * MT ? p.M - m0 : 16 * MT;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
-    const float* wsrow = a.ws + (size_t)(n0 >> 7) * G;      // (16 R divides 128: one scale row)
+    const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(n0 >> 7) * G);      // (16 R divides 128: one row)
 
     f32x4 acc[R][MT];
 #pragma unroll
@@ -92,33 +163,46 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
 #pragma unroll
         for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int per = (G + kWaves - 1) / kWaves;
-    const int g0 = wave * per, g1 = g0 + per < G ? g0 + per : G;
-    for (int g = g0; g < g1; ++g) {
-        u32x4 wf[R][2], xf[MT][2];
-        float f[MT];
-        const uint32_t k = 128u * g + 32u * lq;
+    const int ks = p.ks[at.task];
+    const int b0 = G * at.slice / ks, b1 = G * (at.slice + 1) / ks;
+    const int g0 = b0 + (b1 - b0) * wave / kWaves, g1 = b0 + (b1 - b0) * (wave + 1) / kWaves;
+    for (int gu = g0; gu < g1; gu += U) {
+        u32x4 wf[U][R][2], xf[U][MT][2];
+        float f[U][MT];
 #pragma unroll
-        for (int t = 0; t < R; ++t)
+        for (int j = 0; j < U; ++j) {
+            // a row past the matrix, a column past K and a block past the
+            // wave's last read as zero
+            const int g = gu + j;
+            const bool in = g < g1;
+            const uint32_t k = 128u * g + 16u * lq;     // (chunks lq and 4 + lq: 64 consecutive bytes of a row per load)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)     // a row at or past N, or a column past K, reads as zero
-                wf[t][c] = ld16(rw, k + 16 * c < (uint32_t)K ? (uint32_t)(16 * t + lr) * K + k + 16 * c : 0xFFFFFFF0u);
+            for (int t = 0; t < R; ++t)
 #pragma unroll
-        for (int u = 0; u < MT; ++u) {
+                for (int c = 0; c < 2; ++c)
+                    wf[j][t][c] = ld16(rw, in && k + 64 * c < (uint32_t)K ? (uint32_t)(16 * t + lr) * K + k + 64 * c : 0xFFFFFFF0u);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                xf[u][c] = ld16(rx, k + 16 * c < (uint32_t)K ? (uint32_t)(16 * u + lr) * K + k + 16 * c : 0xFFFFFFF0u);
-            f[u] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(((16 * u + lr) * G + g) * 4), 0, 0));
+            for (int u = 0; u < MT; ++u) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    xf[j][u][c] = ld16(rx, in && k + 64 * c < (uint32_t)K ? (uint32_t)(16 * u + lr) * K + k + 64 * c : 0xFFFFFFF0u);
+                f[j][u] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                        rs, in ? (int)(((16 * u + lr) * G + g) * 4) : (int)0xFFFFFFF0u, 0, 0));
+            }
         }
-        const float s = wsrow[g];
+        __builtin_amdgcn_sched_barrier(0);      // every load is on its way before the first wait
 #pragma unroll
-        for (int u = 0; u < MT; ++u) {
-            const float fs = f[u] * s;
+        for (int j = 0; j < U; ++j) {
+            const float s = wsrow[gu + j < g1 ? gu + j : g1 - 1];
 #pragma unroll
-            for (int t = 0; t < R; ++t) {
-                const f32x4 d = mfma(wf[t], xf[u]);
+            for (int u = 0; u < MT; ++u) {
+                const float fs = f[j][u] * s;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[t][u][v] = __builtin_fmaf(fs, d[v], acc[t][u][v]);
+                for (int t = 0; t < R; ++t) {
+                    const f32x4 d = mfma(wf[j][t], xf[j][u]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[t][u][v] = __builtin_fmaf(fs, d[v], acc[t][u][v]);
+                }
             }
         }
     }
@@ -127,28 +211,23 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
 #pragma unroll
         for (int u = 0; u < MT; ++u) part[wave][t * MT + u][lane] = acc[t][u];
     __syncthreads();
-    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
-    for (int q = wave; q < R * MT; q += kWaves) {
-        f32x4 v = part[0][q][lane];
+    f32x4 v[kMine];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += part[w][q][lane];
-        const int t = q / MT, u = q % MT;
+    for (int j = 0; j < kMine; ++j) {
+        const int q = wave + kWaves * j < kTiles ? wave + kWaves * j : 0;
+        v[j] = part[0][q][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v[j] += part[w][q][lane];
+    }
+    if (ks > 1 && !join(v, p, at, kTiles < kWaves ? kTiles : kWaves, wave, lane, &s_prev)) return;
+    if (wave >= kTiles) return;
+    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int q = wave + kWaves * j, t = q / MT, u = q % MT;
         const int m = m0 + 16 * u + lr, n = n0 + 16 * t + 4 * lq;
-        if (m < p.M && n < a.N) store4(v, a.resid, a.y, a.N, m, n, vec, rvec);
+        if (q < kTiles && m < p.M && n < a.N) store4(v[j], a.resid, a.y, a.N, m, n, vec, rvec);
     }
-}
-
-template <int MT, int R>
-hipError_t launch_rows(const Fp8Args* tasks, int count, int M, hipStream_t s) {
-    Fp8Group p;
-    p.count = count;
-    p.M = M;
-    p.first[0] = 0;
-    for (int i = 0; i < count; ++i) {
-        p.t[i] = tasks[i];
-        p.first[i + 1] = p.first[i] + (tasks[i].N + 16 * R - 1) / (16 * R);
-    }
-    return launch_kernel(fp8_rows_kernel<MT, R>, dim3(p.first[count], (M + 16 * MT - 1) / (16 * MT)), dim3(kWaves * 64), 0, s, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -164,11 +243,6 @@ hipError_t launch_rows(const Fp8Args* tasks, int count, int M, hipStream_t s) {
 // c ^ (r % 8) takes 8.  The swizzle is on the memory side of the load: LDS is
 // written in lane order.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void lds_void;
-// read through the scalar cache (a vector load would join the queue of the
-// loads to LDS, and its wait would wait for all of them)
-typedef const __attribute__((address_space(4))) float const_float;
-
 // Ends a phase of the tile kernel: nothing moves across, no wait is implied.
 __device__ __forceinline__ void phase() {
     __builtin_amdgcn_sched_barrier(0);
@@ -196,21 +270,21 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
 
     // the tile: XCD-contiguous ranges of one task's tiles, walked in
     // super-rows of 8 batch blocks
-    int ti = 0;
-    while (ti + 1 < p.count && (int)blockIdx.x >= p.first[ti + 1]) ++ti;
-    const Fp8Args a = p.t[ti];
+    const Where at0 = where(p, blockIdx.x);
+    const Fp8Args a = p.t[at0.task];
     const int nM = (p.M + BM - 1) / BM, nN = (a.N + BN - 1) / BN;
-    const int T = nM * nN, i = (int)blockIdx.x - p.first[ti], xcd = i & 7, q8 = T >> 3, r8 = T & 7;
-    const int at_tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (i >> 3);
+    const int T = nM * nN, xcd = at0.tile & 7, q8 = T >> 3, r8 = T & 7;
+    const int at_tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (at0.tile >> 3);
     const int per_super = 8 * nN, sup = at_tile / per_super, within = at_tile - sup * per_super;
     const int rows_here = nM - sup * 8 < 8 ? nM - sup * 8 : 8;
     const int m0 = (sup * 8 + within % rows_here) * BM, n0 = within / rows_here * BN;
 
     const int K = a.K, G = (K + 127) >> 7;
     const int rows_m = p.M - m0 < BM ? p.M - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
+    const i32x4 rx = rsrc_words(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
+    const i32x4 rw = rsrc_words(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
+    const i32x4 rs = rsrc_words(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
+    const uint32_t base = lds_address(lds);
     const int nb = (n0 + wn * (BN / WN)) >> 7;
     const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(nb * 128 < a.N ? nb : 0) * G);
 
@@ -228,10 +302,8 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
     auto at = [&](int g) { return g >= G || (tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K) ? 0xFFFF0000u : off; };
     auto piece = [&](int g, uint32_t o, int j) {
         const int i = j < kXLoads ? j : j - kXLoads;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(j < kXLoads ? rx : rw,
-                                                 (lds_void*)(lds + (j < kXLoads ? L::kX + (g & 1) * L::kXStage : L::kW + (g & 1) * L::kWStage) +
-                                                             (wave + kW * i) * 1024),
-                                                 16, (int)o, i * kW * 8 * K + g * 128, 0, 0);
+        to_lds16(j < kXLoads ? rx : rw, o, (uint32_t)(i * kW * 8 * K + g * 128),
+                 base + (j < kXLoads ? L::kX + (g & 1) * L::kXStage : L::kW + (g & 1) * L::kWStage) + (wave + kW * i) * 1024);
     };
     // Scales of blocks 4 q .. 4 q + 3: a row's scales are adjacent, so four
     // cost the lines of one (every block alone: 20 % of the whole kernel).  The
@@ -239,8 +311,7 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
     auto quad_first = [&](int q) { return 4 * q + 4 <= G ? 4 * q : G - 4; };
     auto scales = [&](int g) {
         if ((g & 3) || g >= G || wave >= BM / 64) return;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + L::kS + ((g >> 2) & 1) * L::kQuad + wave * 1024), 16, (int)soff,
-                                                 quad_first(g >> 2) * 4, 0, 0);
+        to_lds16(rs, soff, (uint32_t)quad_first(g >> 2) * 4, base + L::kS + ((g >> 2) & 1) * L::kQuad + wave * 1024);
     };
     auto load = [&](int g) {
         scales(g);
@@ -319,7 +390,6 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
                 if (i >= kAhead) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
                 if (kSecond && i < kN && i % (kN / kLoads) == 0) {
                     piece(g + 2, o, i / (kN / kLoads));
-                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
                 }
             }
             // (the folds stay in this block: sunk into a later one they would cost the overlap)
@@ -355,33 +425,242 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
     tile<BM, BN, WM, WN>(p, lds);
 }
 
-template <int BM, int BN, int WM, int WN>
-hipError_t launch_tile(const Fp8Args* tasks, int count, int M, hipStream_t s) {
-    Fp8Group p;
-    p.count = count;
-    p.M = M;
-    p.first[0] = 0;
-    for (int i = 0; i < count; ++i) {
-        p.t[i] = tasks[i];
-        p.first[i + 1] = p.first[i] + ((M + BM - 1) / BM) * ((tasks[i].N + BN - 1) / BN);
+// ---------------------------------------------------------------------------
+// In between: tiles of BM x BN, S stages in LDS, one barrier per block: block
+// g + S - 1 goes on its way when the waves have left block g - 1, whose stage
+// it takes.  Several workgroups share a CU and fill each other's waits; K may
+// be split over workgroups where the tiles alone are too few.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int S>
+struct MidLds {
+    static constexpr int kXStage = BM * 128, kWStage = BN * 128;
+    static constexpr int kX = 0, kW = S * kXStage, kS = kW + S * kWStage;
+    static constexpr int kQuad = BM * 16, kQuads = (S + 2) / 4 + 1, kBytes = kS + kQuads * kQuad;    // scales of 4 blocks per row
+};
+
+template <int BM, int BN, int WM, int WN, int S>
+__device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s_prev) {
+    using L = MidLds<BM, BN, S>;
+    constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int kXLoads = BM / 8 / kW, kWLoads = BN / 8 / kW, kLoads = kXLoads + kWLoads;
+    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && 128 % (BN / WN) == 0 && BM % 64 == 0 && BM / 64 <= kW && kW % 2 == 0 &&
+                      S >= 2,
+                  "tile");
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const Where at = where(p, blockIdx.x);
+    const Fp8Args a = p.t[at.task];
+    const int nM = (p.M + BM - 1) / BM;
+    const int m0 = at.tile % nM * BM, n0 = at.tile / nM * BN;     // workgroups of one weight block follow each other
+    const int K = a.K, G = (K + 127) >> 7;
+    const int rows_m = p.M - m0 < BM ? p.M - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+    const i32x4 rx = rsrc_words(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
+    const i32x4 rw = rsrc_words(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
+    const i32x4 rs = rsrc_words(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
+    const uint32_t base = lds_address(lds);
+    const int nb = (n0 + wn * (BN / WN)) >> 7;
+    const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(nb * 128 < a.N ? nb : 0) * G);
+
+    // LDS layout, swizzle and zero fill as in the tile kernel
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 4) ^ ((wave & 1) << 2)) * 16u;
+    const uint32_t off = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)K + chunk;
+    const uint32_t soff = (uint32_t)(64 * wave + lane) * (uint32_t)G * 4u;
+    const bool tail = K & 127;
+    const int ks = p.ks[at.task];
+    const int g0 = G * at.slice / ks, g1 = G * (at.slice + 1) / ks;      // (a slice has at least four blocks)
+    auto quad_first = [&](int q) { return 4 * q + 4 <= g1 - g0 ? g0 + 4 * q : g1 - 4; };
+    // block g0 + i into stage i % S; always kLoads loads, and those for the
+    // scales before them, so that vmcnt counts blocks
+    auto load = [&](int i, int stage) {
+        const int g = g0 + i;
+        if (!(i & 3) && g < g1 && wave < BM / 64)
+            to_lds16(rs, soff, (uint32_t)quad_first(i >> 2) * 4, base + L::kS + (i >> 2) % L::kQuads * L::kQuad + wave * 1024);
+        const uint32_t o = g >= g1 || (tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K) ? 0xFFFF0000u : off;
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j)
+            to_lds16(rx, o, (uint32_t)(j * kW * 8 * K + g * 128), base + L::kX + stage * L::kXStage + (wave + kW * j) * 1024);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j)
+            to_lds16(rw, o, (uint32_t)(j * kW * 8 * K + g * 128), base + L::kW + stage * L::kWStage + (wave + kW * j) * 1024);
+    };
+
+    f32x4 acc[TN * TM];
+#pragma unroll
+    for (int i = 0; i < TN * TM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int c0 = ((2 * lq) ^ (lr >> 1)) * 16, c1 = ((2 * lq + 1) ^ (lr >> 1)) * 16;
+    const int xrow = L::kX + (wm * (BM / WM) + lr) * 128, wrow = L::kW + (wn * (BN / WN) + lr) * 128;
+    const int srow = L::kS + (wm * (BM / WM) + lr) * 16;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load(i, i);
+    float next = wsrow[g0];
+    int stage = 0, ahead = S - 1;
+    for (int i = 0; i < g1 - g0; ++i) {
+        constexpr int kBehind = (S - 2) * kLoads;     // loads of the blocks behind block i
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (kBehind & 15) | ((kBehind >> 4) << 14));
+        phase();
+        const float s = next;
+        if (g0 + i + 1 < g1) next = wsrow[g0 + i + 1];
+        const uint8_t* sc = lds + srow + (i >> 2) % L::kQuads * L::kQuad + (g0 + i - quad_first(i >> 2)) * 4;
+        u32x4 xf[TM][2], wf[TN][2];
+        float f[TM];
+#pragma unroll
+        for (int u = 0; u < TM; ++u) {
+            xf[u][0] = *reinterpret_cast<const u32x4*>(lds + xrow + stage * L::kXStage + u * 2048 + c0);
+            xf[u][1] = *reinterpret_cast<const u32x4*>(lds + xrow + stage * L::kXStage + u * 2048 + c1);
+            f[u] = *reinterpret_cast<const float*>(sc + u * 256);
+        }
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            wf[t][0] = *reinterpret_cast<const u32x4*>(lds + wrow + stage * L::kWStage + t * 2048 + c0);
+            wf[t][1] = *reinterpret_cast<const u32x4*>(lds + wrow + stage * L::kWStage + t * 2048 + c1);
+        }
+        __builtin_amdgcn_sched_barrier(0);      // the reads are asked for before the next loads
+        load(i + S - 1, ahead);
+#pragma unroll
+        for (int u = 0; u < TM; ++u) f[u] *= s;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            f32x4 d[TM];
+#pragma unroll
+            for (int u = 0; u < TM; ++u) d[u] = mfma(wf[t], xf[u]);
+#pragma unroll
+            for (int u = 0; u < TM; ++u)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[t * TM + u][v] = __builtin_fmaf(f[u], d[u][v], acc[t * TM + u][v]);
+        }
+        stage = stage + 1 < S ? stage + 1 : 0;
+        ahead = ahead + 1 < S ? ahead + 1 : 0;
+        // this wave's reads of the stage are done before the next barrier lets
+        // it be overwritten
+        __builtin_amdgcn_s_waitcnt(0xC07F);
     }
-    return launch_kernel(fp8_tile_kernel<BM, BN, WM, WN>, dim3(p.first[count]), dim3(64 * WM * WN), 0, s, p);
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // no load to LDS outlives the workgroup
+    if (ks > 1 && !join(acc, p, at, kW, wave, lane, s_prev)) return;
+
+    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+        const int m = m0 + wm * (BM / WM) + 16 * u + lr;
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            const int n = n0 + wn * (BN / WN) + 16 * t + 4 * lq;
+            if (n < a.N) store4(acc[t * TM + u], a.resid, a.y, a.N, m, n, vec, rvec);
+        }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_mid_kernel(Fp8Group p) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[MidLds<BM, BN, S>::kBytes];
+    __shared__ unsigned s_prev;
+    mid<BM, BN, WM, WN, S>(p, lds, &s_prev);
+}
+
+// ---------------------------------------------------------------------------
+// the plan
+// ---------------------------------------------------------------------------
+struct Kind {
+    int bm, bn;             // batch rows and weight rows of a workgroup
+    int waves;              // waves that hand fragments over when K is split
+    bool many;              // several batch tiles: the grid's x carries them (else y)
+    hipError_t (*launch)(const Fp8Group&, dim3, hipStream_t);
+    int frags;              // fragments each of them hands over
+};
+
+template <int MT, int R>
+hipError_t go_rows(const Fp8Group& p, dim3 g, hipStream_t s) {
+    return launch_kernel(fp8_rows_kernel<MT, R>, g, dim3(kWaves * 64), 0, s, p);
+}
+template <int BM, int BN, int WM, int WN, int S>
+hipError_t go_mid(const Fp8Group& p, dim3 g, hipStream_t s) {
+    return launch_kernel(fp8_mid_kernel<BM, BN, WM, WN, S>, g, dim3(64 * WM * WN), 0, s, p);
+}
+template <int BM, int BN, int WM, int WN>
+hipError_t go_tile(const Fp8Group& p, dim3 g, hipStream_t s) {
+    return launch_kernel(fp8_tile_kernel<BM, BN, WM, WN>, g, dim3(64 * WM * WN), 0, s, p);
+}
+template <int MT, int R>
+constexpr Kind rows_kind() { return Kind{16 * MT, 16 * R, R * MT < kWaves ? R * MT : kWaves, false, go_rows<MT, R>, (R * MT + kWaves - 1) / kWaves}; }
+template <int BM, int BN, int WM, int WN, int S>
+constexpr Kind mid_kind() { return Kind{BM, BN, WM * WN, true, go_mid<BM, BN, WM, WN, S>, (BM / WM / 16) * (BN / WN / 16)}; }
+
+struct Plan {
+    const Kind* kind;
+    int ks[kFp8MaxTasks];
+    size_t ws;
+};
+
+int blocks_of(int K) { return (K + 127) / 128; }
+int tiles_of(const Kind& k, int N, int M) { return ((N + k.bn - 1) / k.bn) * (k.many ? (M + k.bm - 1) / k.bm : 1); }
+
+// Bytes of the workspace of a plan's splits (0: none; -1: too many counters).
+size_t plan_ws(const Kind& k, const Fp8Args* t, int count, int M, const int* ks) {
+    size_t part = 0, tiles = 0;
+    for (int i = 0; i < count; ++i)
+        if (ks[i] > 1) {
+            part += (size_t)tiles_of(k, t[i].N, M) * ks[i] * k.waves * k.frags * 1024;
+            tiles += tiles_of(k, t[i].N, M);
+        }
+    if (!part) return 0;
+    return tiles * kCtrStride > kWsCounterBytes ? (size_t)-1 : kWsCounterBytes + part;
+}
+
+static constexpr Kind kRows[4][3] = {{rows_kind<1, 1>(), rows_kind<1, 2>(), rows_kind<1, 4>()},
+                                     {rows_kind<2, 1>(), rows_kind<2, 2>(), rows_kind<2, 4>()},
+                                     {rows_kind<3, 1>(), rows_kind<3, 2>(), rows_kind<3, 4>()},
+                                     {rows_kind<4, 1>(), rows_kind<4, 2>(), rows_kind<4, 4>()}};
+static constexpr Kind kMid[] = {mid_kind<64, 64, 2, 2, 4>(), mid_kind<128, 64, 2, 2, 3>(), mid_kind<128, 128, 2, 2, 2>(),
+                                mid_kind<256, 64, 4, 2, 2>(), mid_kind<64, 64, 2, 2, 8>(), mid_kind<128, 64, 2, 2, 5>(),
+                                mid_kind<128, 128, 2, 2, 4>(), mid_kind<256, 128, 4, 2, 3>(), mid_kind<64, 32, 2, 2, 8>(),
+                                mid_kind<64, 128, 2, 2, 4>(), mid_kind<128, 64, 2, 2, 2>(), mid_kind<64, 64, 2, 2, 3>(),
+                                mid_kind<64, 32, 2, 2, 4>(), mid_kind<64, 128, 2, 2, 3>()};
+static constexpr Kind kTile = {256, 256, 8, true, go_tile<256, 256, 4, 2>, 0};
+
+Plan plan_of(const Fp8Args* t, int count, int M, bool split) {
+    Plan p{};
+    int G = blocks_of(t[0].K);
+    for (int i = 0; i < count; ++i) {
+        p.ks[i] = 1;
+        G = blocks_of(t[i].K) < G ? blocks_of(t[i].K) : G;
+    }
+    // PLAN
+    if (M > 128 && G >= 4) p.kind = &kTile;
+    else p.kind = &kRows[M > 48 ? 3 : (M - 1) / 16][0];
+    p.ws = plan_ws(*p.kind, t, count, M, p.ks);
+    return p;
 }
 
 }  // namespace
 
-size_t fp8_gemm_ws_bytes(const Fp8Args*, int, int) { return 0; }
+size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) { return plan_of(tasks, count, M, true).ws; }
 
-// Fewest 128-column blocks of any task (the tile kernel needs kTileMinBlocks).
-static int min_blocks(const Fp8Args* tasks, int count) {
-    int g = tasks[0].K;
-    for (int i = 1; i < count; ++i) g = tasks[i].K < g ? tasks[i].K : g;
-    return (g + 127) / 128;
-}
-
-hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void*, size_t, hipStream_t s) {
-    if (M > 128 && min_blocks(tasks, count) >= 4) return launch_tile<256, 256, 4, 2>(tasks, count, M, s);
-    return M <= 16 ? launch_rows<1, 1>(tasks, count, M, s) : launch_rows<4, 1>(tasks, count, M, s);
+hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, size_t ws_bytes, hipStream_t s) {
+    Plan plan = plan_of(tasks, count, M, true);
+    if (!ws || ws_bytes < plan.ws) plan = plan_of(tasks, count, M, false);
+    if (plan.ws && (!ws || ws_bytes < plan.ws)) return hipErrorInvalidValue;     // (an unsplit plan needs none)
+    const Kind& k = *plan.kind;
+    Fp8Group p{};
+    p.count = count;
+    p.M = M;
+    p.cnt = static_cast<unsigned*>(ws);
+    p.part = static_cast<uint8_t*>(ws) + (plan.ws ? kWsCounterBytes : 0);
+    uint32_t tile = 0;
+    size_t part = 0;
+    for (int i = 0; i < count; ++i) {
+        const int tiles = tiles_of(k, tasks[i].N, M);
+        p.t[i] = tasks[i];
+        p.ks[i] = plan.ks[i];
+        p.first[i + 1] = p.first[i] + tiles * plan.ks[i];
+        if (plan.ks[i] > 1) {
+            p.tile0[i] = tile;
+            p.part0[i] = part;
+            tile += tiles;
+            part += (size_t)tiles * plan.ks[i] * k.waves * k.frags * 1024;
+        }
+    }
+    return k.launch(p, dim3(p.first[count], k.many ? 1 : (M + k.bm - 1) / k.bm), s);
 }
 
 }  // namespace q4
