@@ -53,31 +53,67 @@ __device__ __forceinline__ f32x4 mfma(const u32x4 (&a)[2], const u32x4 (&b)[2]) 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Rows n .. n + 3 of batch row m: one rounding, the residual added before it.
-// 8-byte accesses where every row start allows them.
-__device__ __forceinline__ void store4(const f32x4& v, const uint16_t* resid, uint16_t* y, int N, int m, int n, bool vec, bool rvec) {
+// The residual is added before the one rounding.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) { return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16); }
+__device__ __forceinline__ bool rows_aligned8(const uint16_t* p, int N) { return (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
+
+// Columns n .. n + 3 of row m, where every row start is 8-byte aligned.
+__device__ __forceinline__ void store4(f32x4 o, const uint16_t* resid, uint16_t* y, int N, int m, int n) {
     const size_t at = (size_t)m * N + n;
-    f32x4 o = v;
     if (resid) {
-        if (rvec && n + 3 < N) {
-            const uint2 r = *reinterpret_cast<const uint2*>(resid + at);
-            o += f32x4{bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y)};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < N) o[i] += __builtin_bit_cast(float, (uint32_t)resid[at + i] << 16);
-        }
+        const uint2 r = *reinterpret_cast<const uint2*>(resid + at);
+        o += f32x4{bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y)};
     }
-    if (vec && n + 3 < N) {
-        *reinterpret_cast<uint2*>(y + at) = make_uint2((uint32_t)f32_to_bf16(o[0]) | ((uint32_t)f32_to_bf16(o[1]) << 16),
-                                                       (uint32_t)f32_to_bf16(o[2]) | ((uint32_t)f32_to_bf16(o[3]) << 16));
-    } else {
+    *reinterpret_cast<uint2*>(y + at) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+}
+
+// 16 rows x W columns from (m, n), in a wave's fragments, to rows at any even
+// address: through LDS (buf: 16 rows of W + 4 floats, the wave's own), so that
+// a store writes consecutive elements.  (Straight from the fragments a store
+// touches 16 rows with 8 bytes each; M = 240, N = 16385, K = 2048: 26.8 us so,
+// 19.1 us at N = 16384.)
+template <int W>
+__device__ __forceinline__ void store_rows(const f32x4* v, int stride, float* buf, const uint16_t* resid, uint16_t* y, int M, int N, int m,
+                                           int n, int lane) {
+    constexpr int kLanes = W < 64 ? W : 64, kRows = 64 / kLanes, kPitch = W + 4;
+    const int lr = lane & 15, lq = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < N) y[at + i] = f32_to_bf16(o[i]);
+    for (int t = 0; t < W / 16; ++t) *reinterpret_cast<f32x4*>(buf + lr * kPitch + 16 * t + 4 * lq) = v[t * stride];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+    for (int r = lane / kLanes; r < 16; r += kRows)
+#pragma unroll
+        for (int c = lane % kLanes; c < W; c += kLanes)
+            if (m + r < M && n + c < N) {
+                const size_t at = (size_t)(m + r) * N + n + c;
+                float o = buf[r * kPitch + c];
+                if (resid) o += __builtin_bit_cast(float, (uint32_t)resid[at] << 16);
+                y[at] = f32_to_bf16(o);
+            }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A wave's TM x TN fragments, rows from m and columns from n on.  lds: free
+// for all waves.
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile(const f32x4* v, uint8_t* lds, const uint16_t* resid, uint16_t* y, int M, int N, int m, int n,
+                                           int wave, int lane) {
+    // v[t * TM + u]: columns n + 16 t + 4 (lane / 16) .. + 3 of row m + 16 u + lane % 16
+    const int lr = lane & 15, lq = lane >> 4;
+    if (rows_aligned8(y, N) && (!resid || rows_aligned8(resid, N))) {
+#pragma unroll
+        for (int u = 0; u < TM; ++u)
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                if (m + 16 * u + lr < M && n + 16 * t + 4 * lq < N)
+                    store4(v[t * TM + u], resid, y, N, m + 16 * u + lr, n + 16 * t + 4 * lq);
+    } else {
+        float* buf = reinterpret_cast<float*>(lds) + wave * 16 * (16 * TN + 4);
+#pragma unroll
+        for (int u = 0; u < TM; ++u)
+            if (m + 16 * u < M) store_rows<16 * TN>(v + u, TM, buf, resid, y, M, N, m + 16 * u, n, lane);
     }
 }
-__device__ __forceinline__ bool rows_aligned8(const uint16_t* p, int N) { return (N & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
 
 struct Fp8Group {
     Fp8Args t[kFp8MaxTasks];
@@ -90,15 +126,29 @@ struct Fp8Group {
     int count, M;
 };
 
-// A workgroup's task, its tile within the task and its slice of K.
+// A workgroup's task, its tile within the task and its slice of K.  Workgroups
+// go to the eight XCDs in turn; each XCD takes a contiguous range of the tiles,
+// so that tiles which share operands share an L2.
 struct Where {
     int task, tile, slice;
 };
 __device__ __forceinline__ Where where(const Fp8Group& p, int block) {
     int t = 0;
     while (t + 1 < p.count && block >= p.first[t + 1]) ++t;
-    const int i = block - p.first[t], ks = p.ks[t];
-    return Where{t, i / ks, i % ks};
+    const int i = block - p.first[t], T = p.first[t + 1] - p.first[t], xcd = i & 7, q8 = T >> 3, r8 = T & 7;
+    const int at = xcd * q8 + (xcd < r8 ? xcd : r8) + (i >> 3), ks = p.ks[t];
+    return Where{t, at / ks, at % ks};
+}
+
+// Batch and weight block of a tile: super-rows of 8 batch blocks, weight block
+// by weight block.
+struct Block {
+    int m, n;
+};
+__device__ __forceinline__ Block block_of(int tile, int nM, int nN) {
+    const int per = 8 * nN, sup = tile / per, within = tile - sup * per;
+    const int here = nM - sup * 8 < 8 ? nM - sup * 8 : 8;
+    return Block{sup * 8 + within % here, within / here};
 }
 
 // Joins the slices of a tile: each of the first `waves` waves stores its NF
@@ -144,6 +194,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
     constexpr int kTiles = R * MT, kMine = (kTiles + kWaves - 1) / kWaves;
     constexpr int U = R * MT <= 4 ? 4 : 2;     // blocks whose loads are in flight together
     __shared__ __attribute__((aligned(16))) f32x4 part[kWaves][kTiles][64];
+    __shared__ __attribute__((aligned(16))) float turn[kWaves][16 * 20];
     __shared__ unsigned s_prev;
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -221,12 +272,11 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
     }
     if (ks > 1 && !join(v, p, at, kTiles < kWaves ? kTiles : kWaves, wave, lane, &s_prev)) return;
     if (wave >= kTiles) return;
-    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-        const int q = wave + kWaves * j, t = q / MT, u = q % MT;
-        const int m = m0 + 16 * u + lr, n = n0 + 16 * t + 4 * lq;
-        if (q < kTiles && m < p.M && n < a.N) store4(v[j], a.resid, a.y, a.N, m, n, vec, rvec);
+        const int q = wave + kWaves * j;
+        if (q < kTiles)
+            store_tile<1, 1>(&v[j], reinterpret_cast<uint8_t*>(turn), a.resid, a.y, p.M, a.N, m0 + 16 * (q % MT), n0 + 16 * (q / MT), wave, lane);
     }
 }
 
@@ -268,17 +318,10 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
 
-    // the tile: XCD-contiguous ranges of one task's tiles, walked in
-    // super-rows of 8 batch blocks
-    const Where at0 = where(p, blockIdx.x);
-    const Fp8Args a = p.t[at0.task];
-    const int nM = (p.M + BM - 1) / BM, nN = (a.N + BN - 1) / BN;
-    const int T = nM * nN, xcd = at0.tile & 7, q8 = T >> 3, r8 = T & 7;
-    const int at_tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (at0.tile >> 3);
-    const int per_super = 8 * nN, sup = at_tile / per_super, within = at_tile - sup * per_super;
-    const int rows_here = nM - sup * 8 < 8 ? nM - sup * 8 : 8;
-    const int m0 = (sup * 8 + within % rows_here) * BM, n0 = within / rows_here * BN;
-
+    const Where where_ = where(p, blockIdx.x);
+    const Fp8Args a = p.t[where_.task];
+    const Block blk = block_of(where_.tile, (p.M + BM - 1) / BM, (a.N + BN - 1) / BN);
+    const int m0 = blk.m * BM, n0 = blk.n * BN;
     const int K = a.K, G = (K + 127) >> 7;
     const int rows_m = p.M - m0 < BM ? p.M - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
     const i32x4 rx = rsrc_words(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
@@ -320,11 +363,9 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
         for (int j = 0; j < kLoads; ++j) piece(g, o, j);
     };
 
-    f32x4 acc[TN][TM];
+    f32x4 acc[TN * TM];
 #pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int u = 0; u < TM; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < TN * TM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int c0 = ((2 * lq) ^ (lr >> 1)) * 16, c1 = ((2 * lq + 1) ^ (lr >> 1)) * 16;
     uint32_t xat[2] = {(uint32_t)(L::kX + (wm * (BM / WM) + lr) * 128 + c0), (uint32_t)(L::kX + (wm * (BM / WM) + lr) * 128 + c1)};
@@ -384,7 +425,7 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
                     const int o = i - kAhead;
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        acc[o / TM][o % TM][v] = __builtin_fmaf(f[o % TM], d[o % (kAhead + 1)][v], acc[o / TM][o % TM][v]);
+                        acc[o][v] = __builtin_fmaf(f[o % TM], d[o % (kAhead + 1)][v], acc[o][v]);
                 }
                 if (i < kN) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 if (i >= kAhead) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
@@ -394,9 +435,7 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
             }
             // (the folds stay in this block: sunk into a later one they would cost the overlap)
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-#pragma unroll
-                for (int u = 0; u < TM; ++u) asm volatile("" : "+v"(acc[t][u]));
+            for (int i = 0; i < TN * TM; ++i) asm volatile("" : "+v"(acc[i]));
             __builtin_amdgcn_s_setprio(0);
             if (!kSecond) __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0)
             if (!kSecond || g + 1 < G) phase();
@@ -406,17 +445,8 @@ __device__ __forceinline__ void tile(const Fp8Group& p, uint8_t* lds) {
     else walk(true);
     __builtin_amdgcn_s_waitcnt(0x0F70);      // no load to LDS outlives the workgroup
 
-    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
-#pragma unroll
-    for (int u = 0; u < TM; ++u) {
-        const int m = m0 + wm * (BM / WM) + 16 * u + lr;
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            const int n = n0 + wn * (BN / WN) + 16 * t + 4 * lq;
-            if (n < a.N) store4(acc[t][u], a.resid, a.y, a.N, m, n, vec, rvec);
-        }
-    }
+    phase();                                 // nor reaches LDS while the epilogue uses it
+    store_tile<TM, TN>(acc, lds, a.resid, a.y, p.M, a.N, m0 + wm * (BM / WM), n0 + wn * (BN / WN), wave, lane);
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -451,8 +481,8 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     const int wm = wave % WM, wn = wave / WM;
     const Where at = where(p, blockIdx.x);
     const Fp8Args a = p.t[at.task];
-    const int nM = (p.M + BM - 1) / BM;
-    const int m0 = at.tile % nM * BM, n0 = at.tile / nM * BN;     // workgroups of one weight block follow each other
+    const Block blk = block_of(at.tile, (p.M + BM - 1) / BM, (a.N + BN - 1) / BN);
+    const int m0 = blk.m * BM, n0 = blk.n * BN;
     const int K = a.K, G = (K + 127) >> 7;
     const int rows_m = p.M - m0 < BM ? p.M - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
     const i32x4 rx = rsrc_words(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
@@ -538,17 +568,8 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     __builtin_amdgcn_s_waitcnt(0x0F70);      // no load to LDS outlives the workgroup
     if (ks > 1 && !join(acc, p, at, kW, wave, lane, s_prev)) return;
 
-    const bool vec = rows_aligned8(a.y, a.N), rvec = a.resid && rows_aligned8(a.resid, a.N);
-#pragma unroll
-    for (int u = 0; u < TM; ++u) {
-        const int m = m0 + wm * (BM / WM) + 16 * u + lr;
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            const int n = n0 + wn * (BN / WN) + 16 * t + 4 * lq;
-            if (n < a.N) store4(acc[t * TM + u], a.resid, a.y, a.N, m, n, vec, rvec);
-        }
-    }
+    phase();
+    store_tile<TM, TN>(acc, lds, a.resid, a.y, p.M, a.N, m0 + wm * (BM / WM), n0 + wn * (BN / WN), wave, lane);
 }
 
 template <int BM, int BN, int WM, int WN, int S>
