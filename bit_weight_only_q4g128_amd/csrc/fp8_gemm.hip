@@ -200,7 +200,8 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Where at = where(p, blockIdx.x);
     const Fp8Args a = p.t[at.task];
-    const int n0 = at.tile * 16 * R, m0 = blockIdx.y * 16 * MT;
+    const Block blk = block_of(at.tile, (p.M + 16 * MT - 1) / (16 * MT), (a.N + 16 * R - 1) / (16 * R));
+    const int n0 = blk.n * 16 * R, m0 = blk.m * 16 * MT;
     const int K = a.K, G = (K + 127) >> 7;
     const int rows_n = a.N - n0 < 16 * R ? a.N - n0 : 16 * R, rows_m = p.M - m0 < 16 * MT ? p.M - m0 : 16 * MT;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
@@ -465,7 +466,8 @@ template <int BM, int BN, int S>
 struct MidLds {
     static constexpr int kXStage = BM * 128, kWStage = BN * 128;
     static constexpr int kX = 0, kW = S * kXStage, kS = kW + S * kWStage;
-    static constexpr int kQuad = BM * 16, kQuads = (S + 2) / 4 + 1, kBytes = kS + kQuads * kQuad;    // scales of 4 blocks per row
+    static constexpr int kScaleWaves = (BM + 63) / 64;
+    static constexpr int kQuad = kScaleWaves * 1024, kQuads = (S + 2) / 4 + 1, kBytes = kS + kQuads * kQuad;    // scales of 4 blocks per row
 };
 
 template <int BM, int BN, int WM, int WN, int S>
@@ -473,7 +475,7 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     using L = MidLds<BM, BN, S>;
     constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kXLoads = BM / 8 / kW, kWLoads = BN / 8 / kW, kLoads = kXLoads + kWLoads;
-    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && 128 % (BN / WN) == 0 && BM % 64 == 0 && BM / 64 <= kW && kW % 2 == 0 &&
+    static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0 && 128 % (BN / WN) == 0 && L::kScaleWaves <= kW && kW % 2 == 0 &&
                       S >= 2,
                   "tile");
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
@@ -504,7 +506,7 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     // scales before them, so that vmcnt counts blocks
     auto load = [&](int i, int stage) {
         const int g = g0 + i;
-        if (!(i & 3) && g < g1 && wave < BM / 64)
+        if (!(i & 3) && g < g1 && wave < L::kScaleWaves)
             to_lds16(rs, soff, (uint32_t)quad_first(i >> 2) * 4, base + L::kS + (i >> 2) % L::kQuads * L::kQuad + wave * 1024);
         const uint32_t o = g >= g1 || (tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K) ? 0xFFFF0000u : off;
 #pragma unroll
@@ -580,14 +582,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_mid_kernel(Fp8Group p) {
 }
 
 // ---------------------------------------------------------------------------
-// the plan
+// the plan: which tile, and how many slices of K
+//
+// The time of a launch is modelled as
+//     fixed + rounds of resident workgroups, each steps x (time of one block)
+// with the per-block times below, measured with 1, 2, ... workgroups on every
+// CU (us; M = 512 .. 4096, K = 2048 and 8192), never less than the bytes at the
+// rate such launches reach, plus the hand-over of a split.  Small tiles fill
+// the CUs early, large ones move fewer bytes per product: at 240 x 8192 x 2048
+// 64 x 64 takes 11.4 us and 256 x 128 21 us, at 4096 x 2048 x 8192 151 and 81.
 // ---------------------------------------------------------------------------
+constexpr int kMaxResident = 4;
 struct Kind {
     int bm, bn;             // batch rows and weight rows of a workgroup
-    int waves;              // waves that hand fragments over when K is split
-    bool many;              // several batch tiles: the grid's x carries them (else y)
+    int waves, frags;       // waves that hand fragments over when K is split, fragments of each
+    int resident;           // workgroups that share a CU
+    float fixed, block[kMaxResident];     // us; block[j]: with j + 1 workgroups on a CU
+    int min_blocks;         // of a slice
     hipError_t (*launch)(const Fp8Group&, dim3, hipStream_t);
-    int frags;              // fragments each of them hands over
 };
 
 template <int MT, int R>
@@ -602,10 +614,27 @@ template <int BM, int BN, int WM, int WN>
 hipError_t go_tile(const Fp8Group& p, dim3 g, hipStream_t s) {
     return launch_kernel(fp8_tile_kernel<BM, BN, WM, WN>, g, dim3(64 * WM * WN), 0, s, p);
 }
-template <int MT, int R>
-constexpr Kind rows_kind() { return Kind{16 * MT, 16 * R, R * MT < kWaves ? R * MT : kWaves, false, go_rows<MT, R>, (R * MT + kWaves - 1) / kWaves}; }
 template <int BM, int BN, int WM, int WN, int S>
-constexpr Kind mid_kind() { return Kind{BM, BN, WM * WN, true, go_mid<BM, BN, WM, WN, S>, (BM / WM / 16) * (BN / WN / 16)}; }
+constexpr Kind mid_kind(int resident, float fixed, float b1, float b2 = 0, float b3 = 0, float b4 = 0) {
+    return Kind{BM, BN, WM * WN, (BM / WM / 16) * (BN / WN / 16), resident, fixed, {b1, b2, b3, b4}, 4, go_mid<BM, BN, WM, WN, S>};
+}
+
+// few rows (no model: see plan_of), any M where a slice of K is short
+const Kind kRows16 = {16, 16, 1, 1, 1, 0, {}, 1, go_rows<1, 1>};
+const Kind kRows32 = {16, 32, 2, 1, 1, 0, {}, 1, go_rows<1, 2>};
+const Kind kRows64 = {64, 32, 8, 1, 1, 0, {}, 1, go_rows<4, 2>};
+const Kind kTiles[] = {
+    mid_kind<32, 32, 2, 2, 4>(4, 3.5f, 0.20f, 0.30f, 0.42f, 0.55f),
+    mid_kind<32, 64, 1, 4, 4>(3, 3.5f, 0.235f, 0.33f, 0.50f),
+    mid_kind<64, 32, 2, 2, 4>(3, 3.5f, 0.25f, 0.335f, 0.52f),
+    mid_kind<64, 64, 2, 2, 4>(2, 4.0f, 0.315f, 0.40f),
+    mid_kind<64, 128, 2, 2, 3>(2, 4.0f, 0.48f, 0.79f),
+    mid_kind<128, 64, 2, 2, 2>(3, 3.0f, 0.69f, 1.03f, 1.21f),
+    mid_kind<128, 128, 2, 2, 2>(2, 3.0f, 1.106f, 1.243f),
+    mid_kind<256, 128, 4, 2, 3>(1, 6.5f, 1.13f),
+    {256, 256, 8, 0, 1, 14.0f, {1.604f}, 4, go_tile<256, 256, 4, 2>},
+};
+constexpr int kCUs = 256;
 
 struct Plan {
     const Kind* kind;
@@ -614,9 +643,10 @@ struct Plan {
 };
 
 int blocks_of(int K) { return (K + 127) / 128; }
-int tiles_of(const Kind& k, int N, int M) { return ((N + k.bn - 1) / k.bn) * (k.many ? (M + k.bm - 1) / k.bm : 1); }
+int tiles_of(const Kind& k, int N, int M) { return ((N + k.bn - 1) / k.bn) * ((M + k.bm - 1) / k.bm); }
 
-// Bytes of the workspace of a plan's splits (0: none; -1: too many counters).
+// Workspace bytes of a plan's splits (0: none), or SIZE_MAX where its tiles
+// have too few counters.
 size_t plan_ws(const Kind& k, const Fp8Args* t, int count, int M, const int* ks) {
     size_t part = 0, tiles = 0;
     for (int i = 0; i < count; ++i)
@@ -625,48 +655,100 @@ size_t plan_ws(const Kind& k, const Fp8Args* t, int count, int M, const int* ks)
             tiles += tiles_of(k, t[i].N, M);
         }
     if (!part) return 0;
-    return tiles * kCtrStride > kWsCounterBytes ? (size_t)-1 : kWsCounterBytes + part;
+    return tiles * kCtrStride > kWsCounterBytes ? SIZE_MAX : kWsCounterBytes + part;
 }
 
-static constexpr Kind kRows[4][3] = {{rows_kind<1, 1>(), rows_kind<1, 2>(), rows_kind<1, 4>()},
-                                     {rows_kind<2, 1>(), rows_kind<2, 2>(), rows_kind<2, 4>()},
-                                     {rows_kind<3, 1>(), rows_kind<3, 2>(), rows_kind<3, 4>()},
-                                     {rows_kind<4, 1>(), rows_kind<4, 2>(), rows_kind<4, 4>()}};
-static constexpr Kind kMid[] = {mid_kind<64, 64, 2, 2, 4>(), mid_kind<128, 64, 2, 2, 3>(), mid_kind<128, 128, 2, 2, 2>(),
-                                mid_kind<256, 64, 4, 2, 2>(), mid_kind<64, 64, 2, 2, 8>(), mid_kind<128, 64, 2, 2, 5>(),
-                                mid_kind<128, 128, 2, 2, 4>(), mid_kind<256, 128, 4, 2, 3>(), mid_kind<64, 32, 2, 2, 8>(),
-                                mid_kind<64, 128, 2, 2, 4>(), mid_kind<128, 64, 2, 2, 2>(), mid_kind<64, 64, 2, 2, 3>(),
-                                mid_kind<64, 32, 2, 2, 4>(), mid_kind<64, 128, 2, 2, 3>()};
-static constexpr Kind kTile = {256, 256, 8, true, go_tile<256, 256, 4, 2>, 0};
+// Modelled time (us) of kind k with up to `split` slices of K per task.
+double plan_time(const Kind& k, const Fp8Args* t, int count, int M, int split, int* ks) {
+    long groups = 0;
+    double steps = 0, work = 0, bytes = 0;
+    for (int i = 0; i < count; ++i) {
+        const int G = blocks_of(t[i].K), tiles = tiles_of(k, t[i].N, M);
+        ks[i] = 1;
+        while (2 * ks[i] <= split && G / (2 * ks[i]) >= k.min_blocks) ks[i] *= 2;
+        const double s = (double)((G + ks[i] - 1) / ks[i]);
+        groups += (long)tiles * ks[i];
+        work += tiles * ks[i] * s;
+        steps = s > steps ? s : steps;
+        bytes += (double)t[i].N * t[i].K + (double)M * t[i].K + 2.0 * M * t[i].N;
+    }
+    // whole rounds of resident workgroups, then the rest; workgroups of
+    // unequal length even out
+    const int r = k.resident;
+    const double mean = work / groups;
+    const long full = groups / (kCUs * r), rest = groups - full * kCUs * r;
+    double run = full * mean * k.block[r - 1];
+    if (rest) run += (full ? mean : steps) * k.block[(rest + kCUs - 1) / kCUs - 1];
+    // a further round fills its stages and stores its tiles anew
+    run += (full + (rest > 0) - 1) * (r == 1 ? k.fixed - 3.5 : 2.0);
+    const double memory = bytes / 4.6e6;
+    const size_t part = plan_ws(k, t, count, M, ks);
+    const double join = part ? 1.8 + 2.0 * (double)part / 8e6 : 0.0;
+    return k.fixed + (run > memory ? run : memory) + join;
+}
 
-Plan plan_of(const Fp8Args* t, int count, int M, bool split) {
+Plan plan_of(const Fp8Args* t, int count, int M, size_t ws_bytes) {
     Plan p{};
     int G = blocks_of(t[0].K);
+    long n = 0;
     for (int i = 0; i < count; ++i) {
         p.ks[i] = 1;
+        n += t[i].N;
         G = blocks_of(t[i].K) < G ? blocks_of(t[i].K) : G;
     }
-    // PLAN
-    if (M > 128 && G >= 4) p.kind = &kTile;
-    else p.kind = &kRows[M > 48 ? 3 : (M - 1) / 16][0];
-    p.ws = plan_ws(*p.kind, t, count, M, p.ks);
+    // Up to one batch tile, and weights that give each CU no more than one such
+    // workgroup (or long rows): the waves load for themselves, with no stages
+    // to fill first (M = 1: N = K = 2048 4.5 us, in tiles 6.2; 8 x 8192 x 8192
+    // 15.9 and 19.0; but N = 16385, K = 2048 11.0 and 9.0).
+    if (M <= 16 && (n <= 32 * kCUs || G >= 32)) {
+        p.kind = n <= 16 * kCUs || n > 32 * kCUs ? &kRows16 : &kRows32;
+        if (n <= 8 * kCUs && G >= 32) {      // half the CUs: two slices (2048 x 8192: 7.2 us, unsplit 7.8)
+            for (int i = 0; i < count; ++i) p.ks[i] = 2;
+            p.ws = plan_ws(*p.kind, t, count, M, p.ks);
+            if (p.ws > ws_bytes) {
+                for (int i = 0; i < count; ++i) p.ks[i] = 1;
+                p.ws = 0;
+            }
+        }
+        return p;
+    }
+    if (G < 4) {
+        p.kind = M <= 16 ? &kRows16 : &kRows64;
+        return p;
+    }
+    double best = 0;
+    for (const Kind& k : kTiles)
+        for (int split = 1; split <= 16; split *= 2) {
+            if (split > 1 && !k.frags) break;
+            int ks[kFp8MaxTasks] = {};
+            const double time = plan_time(k, t, count, M, split, ks);
+            const size_t ws = plan_ws(k, t, count, M, ks);
+            if (ws > ws_bytes || (p.kind && time >= best)) continue;
+            best = time;
+            p.kind = &k;
+            p.ws = ws;
+            for (int i = 0; i < count; ++i) p.ks[i] = ks[i];
+        }
     return p;
 }
 
+// A split's workspace is at most this (a plan that wants more is not made).
+constexpr size_t kMostWs = 48u << 20;
+
 }  // namespace
 
-size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) { return plan_of(tasks, count, M, true).ws; }
+size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) { return plan_of(tasks, count, M, kMostWs).ws; }
 
 hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, size_t ws_bytes, hipStream_t s) {
-    Plan plan = plan_of(tasks, count, M, true);
-    if (!ws || ws_bytes < plan.ws) plan = plan_of(tasks, count, M, false);
-    if (plan.ws && (!ws || ws_bytes < plan.ws)) return hipErrorInvalidValue;     // (an unsplit plan needs none)
+    // (the plan does not depend on how much larger than needed the workspace is)
+    Plan plan = plan_of(tasks, count, M, ws ? kMostWs : 0);
+    if (plan.ws > ws_bytes) plan = plan_of(tasks, count, M, 0);
     const Kind& k = *plan.kind;
     Fp8Group p{};
     p.count = count;
     p.M = M;
-    p.cnt = static_cast<unsigned*>(ws);
-    p.part = static_cast<uint8_t*>(ws) + (plan.ws ? kWsCounterBytes : 0);
+    p.cnt = static_cast<unsigned*>(plan.ws ? ws : nullptr);
+    p.part = plan.ws ? static_cast<uint8_t*>(ws) + kWsCounterBytes : nullptr;
     uint32_t tile = 0;
     size_t part = 0;
     for (int i = 0; i < count; ++i) {
@@ -681,7 +763,7 @@ hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, siz
             part += (size_t)tiles * plan.ks[i] * k.waves * k.frags * 1024;
         }
     }
-    return k.launch(p, dim3(p.first[count], k.many ? 1 : (M + k.bm - 1) / k.bm), s);
+    return k.launch(p, dim3(p.first[count]), s);
 }
 
 }  // namespace q4
