@@ -631,52 +631,55 @@ def mixed_workspace_bytes(items) -> int:
 # 8-bit block-scaled products and the verification of drafted tokens.  These
 # calls may be made while another device than the tensors' is current.
 # ---------------------------------------------------------------------------
-_F32, _I32 = (torch.float32,), (torch.int32,)
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _BLOCK = 128
+# the raw handle of the current stream; building a Stream object costs as much
+# as a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _tensor(t, name: str, dtypes, shape, device):
-    """A contiguous GPU tensor of this shape on this device, or an error that
-    names what is wrong."""
+def _refuse(t, name: str, dtypes, shape, index: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _first(t, name: str, dtypes, ndim: int):
-    _check(t, name, dtypes, ndim)
-    return t.shape, t.device, t.data_ptr()
+def _tensor(t, name: str, dtypes, shape, index: int) -> int:
+    """Address of a contiguous tensor of this shape on GPU `index`, or an error
+    that names what is wrong."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtypes, shape, index)
 
 
-def _optional(t, name: str, dtypes, shape, device):
-    return None if t is None else _tensor(t, name, dtypes, shape, device)
+def _optional(t, name: str, dtypes, shape, index: int):
+    return None if t is None else _tensor(t, name, dtypes, shape, index)
 
 
-def _scratch(workspace, device):
+def _scratch(workspace, index: int):
     if workspace is None:
         return None, 0
-    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+    if workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace.data_ptr(), workspace.numel()
 
 
-def _enqueue(fn, args, device):
-    """fn(*args, stream) on the device's current stream, with that device
-    current (a launch goes to the current device)."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream)
+def _enqueue(index: int, fn, *args):
+    """fn(*args, stream) on GPU index's current stream, with that GPU current (a
+    launch goes to the current device)."""
+    if _get_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise Q4GemvError(rc)
 
@@ -685,42 +688,48 @@ def fp8b128_quantize(x, up=None, codes=None, scale=None):
     """e4m3 codes [M, K] (torch.float8_e4m3fn) and fp32 scales
     [M, ceil(K / 128)] of bf16 activations x, or of silu(x) * up; K a multiple
     of 16.  codes and scale: outputs to write into.  Returns (codes, scale)."""
-    shape, device, xp = _first(x, "x", _U16, 2)
+    _check(x, "x", _U16, 2)
+    shape, index = x.shape, x.get_device()
     M, K = shape
-    upp = _optional(up, "up", _U16, shape, device)
     G = (K + _BLOCK - 1) // _BLOCK
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device)
+        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     if scale is None:
-        scale = torch.empty((M, G), dtype=torch.float32, device=device)
-    cp = _tensor(codes, "codes", _E4M3, shape, device)
-    sp = _tensor(scale, "scale", _F32, (M, G), device)
-    _enqueue(lib.fp8b128_quantize, (xp, upp, M, K, cp, sp), device)
+        scale = x.new_empty((M, G), dtype=torch.float32)
+    _enqueue(index, lib.fp8b128_quantize, x.data_ptr(), _optional(up, "up", _U16, shape, index), M, K,
+             _tensor(codes, "codes", _E4M3, shape, index), _tensor(scale, "scale", _F32, (M, G), index))
     return codes, scale
 
 
 def _fp8_task_array(items):
     items = list(items)
-    if not 1 <= len(items) <= 8:
+    count = len(items)
+    if not 1 <= count <= 8:
         raise ValueError("1..8 tasks per call")
-    arr = (Fp8Task * len(items))()
-    outs, M, device = [], None, None
+    arr = (Fp8Task * count)()
+    outs, M, index = [], None, None
+    last, last_scale = None, None
     for i, (x, x_scale, w, w_scale, residual, out) in enumerate(items):
-        (m, K), dev, xp = _first(x, f"task {i}: x", _E4M3, 2)
-        if M is None:
-            M, device = m, dev
-        elif m != M or dev != device:
-            raise ValueError("all tasks must share the batch size M and the device")
+        if x is not last or x_scale is not last_scale:
+            _check(x, "x", _E4M3, 2)
+            m, K = x.shape
+            if M is None:
+                M, index = m, x.get_device()
+            elif m != M or x.get_device() != index:
+                raise ValueError("all tasks must share the batch size M and the device")
+            G = (K + _BLOCK - 1) // _BLOCK
+            xp, sp = x.data_ptr(), _tensor(x_scale, "x_scale", _F32, (M, G), index)
+            last, last_scale = x, x_scale
         if not isinstance(w, torch.Tensor) or w.dim() != 2:
-            raise ValueError(f"task {i}: w must be a tensor of 2 dims")
-        N, G = w.shape[0], (K + _BLOCK - 1) // _BLOCK
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if out is None else out
+            raise ValueError("w must be a tensor of 2 dims")
+        N = w.shape[0]
+        y = x_scale.new_empty((M, N), dtype=torch.bfloat16) if out is None else out
         outs.append(y)
-        arr[i] = Fp8Task(xp, _tensor(x_scale, "x_scale", _F32, (M, G), device), _tensor(w, "w", _E4M3, (N, K), device),
-                         _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), device),
-                         _optional(residual, "residual", _U16, (M, N), device),
-                         _tensor(y, "out", (torch.bfloat16,), (M, N), device), N, K)
-    return arr, len(items), outs, M, device
+        arr[i] = Fp8Task(xp, sp, _tensor(w, "w", _E4M3, (N, K), index),
+                         _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), index),
+                         _optional(residual, "residual", _U16, (M, N), index),
+                         y.data_ptr() if out is None else _tensor(y, "out", _BF16, (M, N), index), N, K)
+    return arr, count, outs, M, index
 
 
 def fp8b128_gemm_grouped(items, workspace=None):
@@ -733,13 +742,13 @@ def fp8b128_gemm_grouped(items, workspace=None):
     least fp8b128_workspace_bytes(items) bytes, zero-filled before its first
     use and reusable afterwards without clearing (lets few rows split K).
     Returns the list of outputs."""
-    arr, count, outs, M, device = _fp8_task_array(items)
-    wp, wn = _scratch(workspace, device)
-    _enqueue(lib.fp8b128_gemm_grouped_ws, (arr, count, M, wp, wn), device)
+    arr, count, outs, M, index = _fp8_task_array(items)
+    _enqueue(index, lib.fp8b128_gemm_grouped_ws, arr, count, M, *_scratch(workspace, index))
     return outs
 
 
 def fp8b128_workspace_bytes(items) -> int:
+    """Bytes of workspace fp8b128_gemm_grouped can use for these items (0: none)."""
     arr, count, _, M, _ = _fp8_task_array(items)
     n = ctypes.c_size_t(0)
     _raise(lib.fp8b128_workspace_bytes(arr, count, M, ctypes.byref(n)))
@@ -749,7 +758,7 @@ def fp8b128_workspace_bytes(items) -> int:
 def fp8b128_gemm(x, x_scale, w, w_scale, residual=None, out=None, workspace=None):
     """y[M, N] = sum over blocks of 128 columns of x_scale * w_scale * (x . W^T)
     (+ residual), bf16: one product of fp8b128_gemm_grouped."""
-    return fp8b128_gemm_grouped([(x, x_scale, w, w_scale, residual, out)], workspace)[0]
+    return fp8b128_gemm_grouped(((x, x_scale, w, w_scale, residual, out),), workspace)[0]
 
 
 def verify_topk_workspace_bytes(B: int, D: int, V: int, top_k: int = 30) -> int:
@@ -762,21 +771,6 @@ def verify_full_workspace_bytes(B: int, D: int, V: int) -> int:
     return int(lib.q4_verify_full_workspace_bytes(B, D, V))
 
 
-def _verify_outputs(logits, draft, u, n_draft, need, workspace):
-    (B, D1, V), device, lp = _first(logits, "logits", _U16, 3)
-    D = D1 - 1
-    dp = _tensor(draft, "draft", _I32, (B, D), device)
-    up = _tensor(u, "u", _F32, (B, D1), device)
-    np_ = _optional(n_draft, "n_draft", _I32, (B,), device)
-    if workspace is None:
-        workspace = torch.empty(need(B, D, V), dtype=torch.uint8, device=device)
-    wp, wn = _scratch(workspace, device)
-    token = torch.empty((B, D1), dtype=torch.int32, device=device)
-    count = torch.empty((B,), dtype=torch.int32, device=device)
-    prob = torch.empty((B, D), dtype=torch.float32, device=device)
-    return B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob
-
-
 def verify_topk(logits, draft, u, draft_index=None, draft_prob=None, n_draft=None, temperature: float = 0.8, top_k: int = 30,
                 workspace=None):
     """Verifies drafted tokens against the target's top-k distributions
@@ -784,20 +778,29 @@ def verify_topk(logits, draft, u, draft_index=None, draft_prob=None, n_draft=Non
     [B, D], u fp32 [B, D + 1] in [0, 1) (D acceptance uniforms, then the
     draw's), the draft's distributions as draft_index int32 and draft_prob fp32
     [B, D, k'] (sample_topk's outputs) or None for a draft certain of its
-    tokens, n_draft int32 [B] or None.  Returns (token int32 [B, D + 1]: the
-    tokens that stand, the one drawn after them, then -1; count int32 [B]: how
-    many stand; accept_prob fp32 [B, D])."""
-    B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob = _verify_outputs(
-        logits, draft, u, n_draft, lambda b, d, v: verify_topk_workspace_bytes(b, d, v, top_k), workspace)
+    tokens, n_draft int32 [B] or None.  workspace: uint8, at least
+    verify_topk_workspace_bytes (None: one is allocated); it needs no clearing.
+    Returns (token int32 [B, D + 1]: the tokens that stand, the one drawn after
+    them, then -1; count int32 [B]: how many stand; accept_prob fp32 [B, D])."""
+    _check(logits, "logits", _U16, 3)
+    B, D1, V = logits.shape
+    D, index = D1 - 1, logits.get_device()
+    if workspace is None:
+        workspace = logits.new_empty(verify_topk_workspace_bytes(B, D, V, top_k), dtype=torch.uint8)
     kd = 0
     if draft_index is not None:
         if not isinstance(draft_index, torch.Tensor) or draft_index.dim() != 3:
             raise ValueError("draft_index must be a tensor of 3 dims")
         kd = draft_index.shape[2]
-    ip = _optional(draft_index, "draft_index", _I32, (B, D, kd), device)
-    pp = _optional(draft_prob, "draft_prob", _F32, (B, D, kd), device)
-    _enqueue(lib.q4_verify_topk, (lp, B, D, V, dp, ip, pp, kd, np_, up, temperature, top_k, token.data_ptr(), count.data_ptr(),
-                                  prob.data_ptr(), wp, wn), device)
+    up = _tensor(u, "u", _F32, (B, D1), index)
+    token = u.new_empty((B, D1), dtype=torch.int32)
+    count = u.new_empty(B, dtype=torch.int32)
+    prob = u.new_empty((B, D))
+    _enqueue(index, lib.q4_verify_topk, logits.data_ptr(), B, D, V, _tensor(draft, "draft", _I32, (B, D), index),
+             _optional(draft_index, "draft_index", _I32, (B, D, kd), index),
+             _optional(draft_prob, "draft_prob", _F32, (B, D, kd), index), kd, _optional(n_draft, "n_draft", _I32, (B,), index),
+             up, temperature, top_k, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
+             *_scratch(workspace, index))
     return token, count, prob
 
 
@@ -805,9 +808,17 @@ def verify_full(logits, draft, u, draft_logits=None, n_draft=None, temperature: 
     """Verifies drafted tokens against the softmax of whole rows
     (q4_verify_full in the C header): as verify_topk, with the draft's
     distributions as draft_logits bf16 [B, D, V] or None."""
-    B, D, V, device, lp, dp, up, np_, wp, wn, token, count, prob = _verify_outputs(logits, draft, u, n_draft,
-                                                                                   verify_full_workspace_bytes, workspace)
-    qp = _optional(draft_logits, "draft_logits", _U16, (B, D, V), device)
-    _enqueue(lib.q4_verify_full, (lp, B, D, V, dp, qp, np_, up, temperature, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
-                                  wp, wn), device)
+    _check(logits, "logits", _U16, 3)
+    B, D1, V = logits.shape
+    D, index = D1 - 1, logits.get_device()
+    if workspace is None:
+        workspace = logits.new_empty(verify_full_workspace_bytes(B, D, V), dtype=torch.uint8)
+    up = _tensor(u, "u", _F32, (B, D1), index)
+    token = u.new_empty((B, D1), dtype=torch.int32)
+    count = u.new_empty(B, dtype=torch.int32)
+    prob = u.new_empty((B, D))
+    _enqueue(index, lib.q4_verify_full, logits.data_ptr(), B, D, V, _tensor(draft, "draft", _I32, (B, D), index),
+             _optional(draft_logits, "draft_logits", _U16, (B, D, V), index), _optional(n_draft, "n_draft", _I32, (B,), index),
+             up, temperature, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
+             *_scratch(workspace, index))
     return token, count, prob
