@@ -779,7 +779,8 @@ def verify_topk(logits, draft, u, draft_index=None, draft_prob=None, n_draft=Non
     draw's), the draft's distributions as draft_index int32 and draft_prob fp32
     [B, D, k'] (sample_topk's outputs) or None for a draft certain of its
     tokens, n_draft int32 [B] or None.  workspace: uint8, at least
-    verify_topk_workspace_bytes (None: one is allocated); it needs no clearing.
+    verify_topk_workspace_bytes, zero-filled before its first use and reusable
+    afterwards without clearing (None: one is made for the call).
     Returns (token int32 [B, D + 1]: the tokens that stand, the one drawn after
     them, then -1; count int32 [B]: how many stand; accept_prob fp32 [B, D])."""
     _check(logits, "logits", _U16, 3)
@@ -812,7 +813,7 @@ def verify_full(logits, draft, u, draft_logits=None, n_draft=None, temperature: 
     B, D1, V = logits.shape
     D, index = D1 - 1, logits.get_device()
     if workspace is None:
-        workspace = logits.new_empty(verify_full_workspace_bytes(B, D, V), dtype=torch.uint8)
+        workspace = logits.new_zeros(verify_full_workspace_bytes(B, D, V), dtype=torch.uint8)
     up = _tensor(u, "u", _F32, (B, D1), index)
     token = u.new_empty((B, D1), dtype=torch.int32)
     count = u.new_empty(B, dtype=torch.int32)

@@ -31,22 +31,33 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 2^y by the Taylor series of 2^f on |f| <= 1/2 (relative error 7e-12); y
-// below -1100, and NaN, give 0.
+// 2^y for y >= -1000 (below, and for NaN: 2^-1000): y = n + f, |f| <= 1/2,
+// with n from the low word of y + 1.5 * 2^52, and 2^f by the polynomial of
+// degree 8 with the least largest relative error on the interval (8e-13,
+// fitted by reweighted least squares).  Conversions to integer and ldexp, which
+// run at a fraction of the fp64 rate, are not needed.
+__device__ __forceinline__ double exp2_raw(double y) {
+    constexpr double kShift = 6755399441055744.0;
+    y = __builtin_fmax(y, -1000.0);
+    const double k = y + kShift, f = y - (k - kShift);
+    double p = 1.3175848283035606e-06;
+    p = __builtin_fma(p, f, 1.5309737450565635e-05);
+    p = __builtin_fma(p, f, 1.5403851794620636e-04);
+    p = __builtin_fma(p, f, 1.3333452062188023e-03);
+    p = __builtin_fma(p, f, 9.6181285427970660e-03);
+    p = __builtin_fma(p, f, 5.5504109393417454e-02);
+    p = __builtin_fma(p, f, 2.4022650698880670e-01);
+    p = __builtin_fma(p, f, 6.9314718054651500e-01);
+    p = __builtin_fma(p, f, 9.9999999999976290e-01);
+    // (in assembly: the compiler makes five instructions of this addition)
+    uint2 w = __builtin_bit_cast(uint2, p);
+    asm("v_lshl_add_u32 %0, %1, 20, %0" : "+v"(w.y) : "v"(__builtin_bit_cast(uint2, k).x));
+    return __builtin_bit_cast(double, w);
+}
+// The same with 0 below.
 __device__ __forceinline__ double exp2_64(double y) {
-    y = __builtin_fmax(y, -1100.0);
-    const double n = __builtin_rint(y), f = y - n;
-    double p = 1.0178086009239699e-07;                       // (ln 2)^9 / 9!
-    p = __builtin_fma(p, f, 1.3215486790144307e-06);
-    p = __builtin_fma(p, f, 1.5252733804059841e-05);
-    p = __builtin_fma(p, f, 1.5403530393381608e-04);
-    p = __builtin_fma(p, f, 1.3333558146428443e-03);
-    p = __builtin_fma(p, f, 9.6181291076284770e-03);
-    p = __builtin_fma(p, f, 5.5504108664821580e-02);
-    p = __builtin_fma(p, f, 2.4022650695910072e-01);
-    p = __builtin_fma(p, f, 6.9314718055994531e-01);
-    p = __builtin_fma(p, f, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    const double v = exp2_raw(y);
+    return y > -1000.0 ? v : 0.0;
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -219,15 +230,18 @@ __global__ __launch_bounds__(kTopkWaves * 64) void verify_topk_kernel(VerifyArgs
 }
 
 // ---------------------------------------------------------------------------
-// whole form: a launch for the masses of all rows, one for the acceptance and
-// the draw.
+// whole form.  First launch: the masses of all rows, in chunks; the workgroup
+// that ends a sequence's last chunk verifies its drafted tokens.  Second
+// launch: the sums of max(p - q, 0) and of p over the chunks of each sequence's
+// stop row; the last one finds the chunk, then the entry, that the draw hits.
 //
 // A row starts at any even address.  It is read as the 16-byte aligned groups
 // of 8 logits that touch it; the first and the last, where the row ends inside
 // them, value by value.
 // ---------------------------------------------------------------------------
-constexpr int kMassGroups = 1024;      // groups of 8 logits per workgroup of the first launch
-constexpr int kDrawGroups = 512;       // of the second: 2 adjacent groups per thread
+constexpr int kMassJ = 4;      // groups of 8 logits per thread of the first launch (1 where the workgroups are few)
+constexpr int kDrawJ = 2;      // of the second, adjacent ones (likewise)
+constexpr int kSequences = (int)(kWsCounterBytes / kCtrStride);      // sequences of one pair of launches
 
 struct Row {
     const uint16_t* p;     // first logit
@@ -237,54 +251,162 @@ __device__ __forceinline__ Row row_of(const uint16_t* p, int V) {
     const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15) >> 1);
     return Row{p, off, (off + V + 7) >> 3};
 }
-__host__ __device__ constexpr int row_groups_most(int V) { return (V + 14) >> 3; }
+// Most groups of any row: rows that all start on 16 bytes touch none twice.
+size_t row_groups(int V, bool aligned) { return aligned ? (size_t)V >> 3 : ((size_t)V + 14) >> 3; }
 
-// The 8 logits of group g as fp32, -inf where the group lies outside the row.
-__device__ __forceinline__ void load_group(const Row& r, int V, int g, float (&z)[8]) {
-    const int i0 = 8 * g - r.off;
-    if (i0 >= 0 && i0 + 8 <= V) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(r.p + i0);
+// Groups g[0 .. NJ) as bf16 pairs, -inf outside the row.  The loads of groups
+// that lie in the row whole (the others take such a one's address) are all on
+// their way before the few lanes with a row's end in a group read it value by
+// value.
+template <int NJ>
+__device__ __forceinline__ void load_groups(const Row& r, int V, const int (&g)[NJ], u32x4 (&v)[NJ]) {
+    constexpr uint32_t kNone = 0xFF80FF80u;
+    const int lo = r.off ? 1 : 0, hi = (r.off + V) >> 3;      // whole groups: lo .. hi - 1
+    bool edge = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            z[2 * i] = bf16lo(v[i]);
-            z[2 * i + 1] = bf16hi(v[i]);
-        }
-    } else {
+    for (int j = 0; j < NJ; ++j) {
+        const int at = g[j] < lo ? lo : g[j] >= hi ? hi - 1 : g[j];
+        edge = edge || at != g[j];
+        v[j] = hi > lo ? *reinterpret_cast<const u32x4*>(r.p + 8 * at - r.off) : u32x4{kNone, kNone, kNone, kNone};
+    }
+    if (!edge) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = i0 + i >= 0 && i0 + i < V;
-            z[i] = in ? __builtin_bit_cast(float, (uint32_t)r.p[in ? i0 + i : 0] << 16) : -__builtin_huge_valf();
+    for (int j = 0; j < NJ; ++j) {
+        if (g[j] >= lo && g[j] < hi) continue;
+        const int i0 = 8 * g[j] - r.off;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 2 * e;
+            const uint32_t a = i >= 0 && i < V ? r.p[i] : 0xFF80u, b = i + 1 >= 0 && i + 1 < V ? r.p[i + 1] : 0xFF80u;
+            v[j][e] = a | (b << 16);
         }
     }
 }
+__device__ __forceinline__ float half_of(const u32x4& v, int e) { return e & 1 ? bf16hi(v[e >> 1]) : bf16lo(v[e >> 1]); }
 
 struct Mass {       // sum of 2^((z - top) c) and top of a part of a row
     double sum;
     double top;
 };
 
-// Block (row, chunk): rows are the target's B (D + 1), then the draft's B D.
-// The first block of a sequence clears the counter of the second launch.
-__global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int chunks, double c, Mass* mass, unsigned* cnt) {
+// The mass of a whole row from its parts, by 16 adjacent lanes (all of them
+// get it); sum 0 for a row without a distribution.
+__device__ __forceinline__ Mass row_mass(Mass* part, int chunks, double c, int lane) {
+    double sum = 0.0;
+    float top = -__builtin_huge_valf();
+    for (int i0 = 0; i0 < chunks; i0 += 64) {          // 4 parts per lane at a time
+        double s[4];
+        float t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 16 * j + (lane & 15);
+            s[j] = i < chunks ? get(&part[i].sum) : 0.0;
+            t[j] = i < chunks ? (float)get(&part[i].top) : -__builtin_huge_valf();       // (bf16 values)
+        }
+        float m = top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = fmaxf(m, t[j]);
+#pragma unroll
+        for (int k = 1; k < 16; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+        sum *= exp2_64(((double)top - (double)m) * c);      // (0 * 0 at first)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += s[j] * exp2_64(((double)t[j] - (double)m) * c);
+        top = m;
+    }
+#pragma unroll
+    for (int k = 1; k < 16; k *= 2) sum += __shfl_xor(sum, k);
+    const bool some = top > -__builtin_huge_valf() && top < __builtin_huge_valf();
+    return some ? Mass{sum, (double)top} : Mass{0.0, 0.0};
+}
+
+// p = 2^((z - top) c) inv; inv = 1 / sum, or 0 for a row without a distribution
+__device__ __forceinline__ double inverse(const Mass& m) { return m.sum > 0.0 ? 1.0 / m.sum : 0.0; }
+__device__ __forceinline__ double prob(float z, double top, double inv, double c) { return exp2_64(((double)z - top) * c) * inv; }
+
+// Where a sequence stops, and the distributions there.
+struct Stop {
+    double p_top, p_inv, q_top, q_inv;
+    int stand, has_q, qtoken;      // has_q: the draft's logits give q; else q = 1 at qtoken (-1: nowhere)
+    int pad;
+};
+
+// Sequence b: accepts, writes everything but the drawn token.
+__device__ __forceinline__ void accept(const VerifyArgs& a, int b, int n, int chunks, double c, Mass* mass, Stop* stop, int tid) {
+    __shared__ Mass s_mass[2 * kMaxDraft + 1];
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), D = a.D, V = a.V;
+    // lane i of wave 0: drafted token i, its logits asked for first
+    int d = -1;
+    uint32_t zd = 0, yd = 0;
+    float ui = 0.f;
+    if (wave == 0 && lane < n) {
+        d = a.draft[(size_t)b * D + lane];
+        ui = a.u[(size_t)b * (D + 1) + lane];
+        if (d >= 0 && d < V) {
+            zd = a.logits[((size_t)b * (D + 1) + lane) * V + d];
+            if (a.draft_logits) yd = a.draft_logits[((size_t)b * D + lane) * V + d];
+        }
+    }
+    // target rows 0 .. n, draft rows 0 .. n - 1, in the order of their masses
+    const int rows = n + 1 + (a.draft_logits ? n : 0);
+    for (int i0 = 4 * wave; i0 < rows; i0 += 16) {
+        const int i = i0 + (lane >> 4) < rows ? i0 + (lane >> 4) : rows - 1;
+        const Mass m = row_mass(mass + (size_t)(i <= n ? i : D + 1 + (i - n - 1)) * chunks, chunks, c, lane);
+        if ((lane & 15) == 0) s_mass[i] = m;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        bool ok = false;
+        if (lane < n) {
+            const bool in = d >= 0 && d < V;
+            double pd = 0.0, qd = in ? 1.0 : 0.0;
+            if (in) {
+                pd = prob(__builtin_bit_cast(float, zd << 16), s_mass[lane].top, inverse(s_mass[lane]), c);
+                if (a.draft_logits)
+                    qd = prob(__builtin_bit_cast(float, yd << 16), s_mass[n + 1 + lane].top, inverse(s_mass[n + 1 + lane]), c);
+            }
+            ok = (double)ui * qd < pd;
+            if (a.accept_prob) a.accept_prob[(size_t)b * D + lane] = accept_ratio(pd, qd);
+        } else if (lane < D && a.accept_prob) {
+            a.accept_prob[(size_t)b * D + lane] = 0.f;
+        }
+        const int stand = (int)__builtin_ctzll(~__ballot(ok));          // (lanes n .. 63 are never ok, and n <= 63)
+        const bool refused = stand < n, has_q = refused && a.draft_logits;
+        const int at = __shfl(d, stand);
+        if (lane == 0) {
+            const Mass pm = s_mass[stand], qm = has_q ? s_mass[n + 1 + stand] : Mass{0.0, 0.0};
+            *stop = Stop{pm.top, inverse(pm), qm.top, inverse(qm), stand, has_q, refused && !has_q ? at : -1, 0};
+            a.count[b] = stand;
+        }
+        if (lane <= D && lane != stand) a.token[(size_t)b * (D + 1) + lane] = lane < stand ? d : -1;
+    }
+}
+
+// Block (sequence, row, chunk); a sequence's rows are the target's D + 1, then
+// the draft's D.
+template <int J>
+__global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int rows, int chunks, double c, Mass* mass, unsigned* cnt,
+                                                            Stop* stop) {
     __shared__ float s_top[4];
     __shared__ double s_sum[4];
+    __shared__ unsigned s_prev;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-    const int targets = a.B * (a.D + 1);
-    const bool target = row < targets;
-    const int per = target ? a.D + 1 : a.D, at = target ? row : row - targets;
-    const int b = at / per, i = at - b * per;
-    if (target && i == 0 && chunk == 0 && tid == 0) cnt[(size_t)b * kCtrWords] = 0;
-    if (i >= drafted(a, b) + (target ? 1 : 0)) return;
-    const Row r = row_of((target ? a.logits : a.draft_logits) + (size_t)at * a.V, a.V);
-    float z[4][8];
+    const int b = blockIdx.x / (rows * chunks), rest = blockIdx.x - b * rows * chunks;
+    const int i = rest / chunks, chunk = rest - i * chunks;
+    const int n = drafted(a, b);
+    const bool target = i <= a.D;
+    if (target ? i > n : i - a.D - 1 >= n) return;                     // no drafted token leads here
+    const Row r = row_of(target ? a.logits + ((size_t)b * (a.D + 1) + i) * a.V : a.draft_logits + ((size_t)b * a.D + (i - a.D - 1)) * a.V,
+                         a.V);
+    u32x4 v[J];
+    int at[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) at[j] = (chunk * J + j) * kThreads + tid;
+    load_groups<J>(r, a.V, at, v);
     float top = -__builtin_huge_valf();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_group(r, a.V, chunk * kMassGroups + j * kThreads + tid, z[j]);
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, z[j][e]);
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, half_of(v[j], e));
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
     if (lane == 0) s_top[wave] = top;
@@ -293,130 +415,83 @@ __global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int ch
     double sum = 0.0;
     const double base = -(double)top * c;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += exp2_64(__builtin_fma((double)z[j][e], c, base));
+        for (int e = 0; e < 8; ++e) sum += exp2_raw(__builtin_fma((double)half_of(v[j], e), c, base));
     sum = wave_sum(sum);
     if (lane == 0) s_sum[wave] = sum;
     __syncthreads();
-    if (tid == 0) mass[(size_t)row * chunks + chunk] = Mass{s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3], (double)top};
-}
-
-// The mass of a whole row from its parts (a wave); sum 0 for a row without a
-// distribution.
-__device__ __forceinline__ Mass row_mass(const Mass* part, int chunks, double c, int lane) {
-    double top = -__builtin_huge_val();
-    for (int i = lane; i < chunks; i += 64) top = __builtin_fmax(top, part[i].top);
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) top = __builtin_fmax(top, __shfl_xor(top, s));
-    if (!(top > -__builtin_huge_val() && top < __builtin_huge_val())) return Mass{0.0, 0.0};
-    double sum = 0.0;
-    for (int i = lane; i < chunks; i += 64) sum += part[i].sum * exp2_64((part[i].top - top) * c);
-    return Mass{wave_sum(sum), top};
-}
-
-__device__ __forceinline__ double prob(float z, const Mass& m, double inv, double c) {
-    return exp2_64(((double)z - m.top) * c) * inv;      // inv = 1 / sum, or 0 for a row without a distribution
+    Mass* mine = mass + (size_t)b * rows * chunks;
+    if (tid == 0) {
+        put(&mine[rest].sum, s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
+        put(&mine[rest].top, (double)top);
+    }
+    const int active = n + 1 + (a.draft_logits ? n : 0);
+    if (!arrive_last(cnt + (size_t)b * kCtrWords, active * chunks, tid, &s_prev)) return;
+    accept(a, b, n, chunks, c, mine, stop + b, tid);
 }
 
 struct Part {
     double rest, all;    // sums of max(p - q, 0) and of p over a chunk
 };
 
-// The stop row's values of a thread's 16 adjacent logits.
+// The stop row's values of a thread's 8 J adjacent logits.
+template <int J>
 struct Values {
-    double rest[16], all[16];
+    double rest[8 * J], all[8 * J];
 };
-__device__ __forceinline__ void stop_values(const VerifyArgs& a, const Row& tr, const Row& dr, bool has_q, int qtoken, const Mass& pm,
-                                            double pinv, const Mass& qm, double qinv, double c, int g0, Values& o) {
-    float z[8], y[8];
+template <int J>
+__device__ __forceinline__ void stop_values(const VerifyArgs& a, const Row& tr, const Row& dr, const Stop& st, double c, int g0, Values<J>& o) {
+    u32x4 z[J], y[J];
+    int g[J];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        load_group(tr, a.V, g0 + j, z);
-        const int i0 = 8 * (g0 + j) - tr.off;
+    for (int j = 0; j < J; ++j) g[j] = g0 + j;
+    load_groups<J>(tr, a.V, g, z);
+    if (st.has_q) {
+        if (dr.off == tr.off) {
+            load_groups<J>(dr, a.V, g, y);
+        } else {        // the draft's row starts at another place of its group
+            uint32_t h[8 * J];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double p = prob(z[e], pm, pinv, c);
-            o.all[8 * j + e] = p;
-            o.rest[8 * j + e] = i0 + e == qtoken ? 0.0 : p;
-        }
-        if (has_q) {
-            if (dr.off == tr.off) {
-                load_group(dr, a.V, g0 + j, y);
-            } else {        // the draft's row starts at another place of its group
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = i0 + e;
-                    const bool in = i >= 0 && i < a.V;
-                    y[e] = in ? __builtin_bit_cast(float, (uint32_t)dr.p[in ? i : 0] << 16) : -__builtin_huge_valf();
-                }
+            for (int e = 0; e < 8 * J; ++e) {
+                const int i = 8 * g0 - tr.off + e;
+                h[e] = dr.p[i < 0 ? 0 : i < a.V ? i : a.V - 1];       // (outside the row p is 0, whatever q)
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.rest[8 * j + e] = __builtin_fmax(o.all[8 * j + e] - prob(y[e], qm, qinv, c), 0.0);
+            for (int e = 0; e < 4 * J; ++e) y[e >> 2][e & 3] = h[2 * e] | (h[2 * e + 1] << 16);
         }
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double p = prob(half_of(z[j], e), st.p_top, st.p_inv, c);
+            o.all[8 * j + e] = p;
+            if (st.has_q) o.rest[8 * j + e] = __builtin_fmax(p - prob(half_of(y[j], e), st.q_top, st.q_inv, c), 0.0);
+            else o.rest[8 * j + e] = 8 * (g0 + j) - tr.off + e == st.qtoken ? 0.0 : p;
+        }
 }
 
 // Block (b, chunk).
-__global__ __launch_bounds__(kThreads) void verify_full_kernel(VerifyArgs a, int mass_chunks, int chunks, double c, const Mass* mass,
-                                                               unsigned* cnt, Part* parts) {
-    __shared__ Mass s_mass[2 * kMaxDraft + 1];
+template <int J>
+__global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int chunks, double c, const Stop* stop, unsigned* cnt, Part* parts) {
     __shared__ double s_wave[2][4];
     __shared__ unsigned s_prev;
-    __shared__ int s_stand, s_token, s_chunk;
+    __shared__ int s_rest, s_chunk, s_first[4], s_last[4];
     __shared__ double s_before, s_x;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.x / chunks, chunk = blockIdx.x - b * chunks;
-    const int n = drafted(a, b), D = a.D, V = a.V;
-    const int targets = a.B * (D + 1);
+    const int D = a.D, V = a.V;
+    const Stop st = stop[b];
+    const Row tr = row_of(a.logits + ((size_t)b * (D + 1) + st.stand) * V, V);
+    const Row dr = st.has_q ? row_of(a.draft_logits + ((size_t)b * D + st.stand) * V, V) : tr;
 
-    // the masses of the sequence's rows: target 0 .. n, draft 0 .. n - 1
-    const int rows = n + 1 + (a.draft_logits ? n : 0);
-    for (int i = wave; i < rows; i += 4) {
-        const size_t row = i <= n ? (size_t)b * (D + 1) + i : (size_t)targets + (size_t)b * D + (i - n - 1);
-        const Mass m = row_mass(mass + row * mass_chunks, mass_chunks, c, lane);
-        if (lane == 0) s_mass[i] = m;
-    }
-    __syncthreads();
-    if (wave == 0) {        // lane i: drafted token i
-        bool ok = false;
-        if (lane < n) {
-            const int d = a.draft[(size_t)b * D + lane];
-            const bool in = d >= 0 && d < V;
-            double pd = 0.0, qd = in ? 1.0 : 0.0;
-            if (in) {
-                const Mass m = s_mass[lane];
-                const uint32_t z = a.logits[((size_t)b * (D + 1) + lane) * V + d];
-                pd = prob(__builtin_bit_cast(float, z << 16), m, m.sum > 0.0 ? 1.0 / m.sum : 0.0, c);
-                if (a.draft_logits) {
-                    const Mass w = s_mass[n + 1 + lane];
-                    const uint32_t y = a.draft_logits[((size_t)b * D + lane) * V + d];
-                    qd = prob(__builtin_bit_cast(float, y << 16), w, w.sum > 0.0 ? 1.0 / w.sum : 0.0, c);
-                }
-            }
-            ok = (double)a.u[(size_t)b * (D + 1) + lane] * qd < pd;
-            if (a.accept_prob && chunk == 0) a.accept_prob[(size_t)b * D + lane] = accept_ratio(pd, qd);
-        } else if (lane < D && a.accept_prob && chunk == 0) {
-            a.accept_prob[(size_t)b * D + lane] = 0.f;
-        }
-        const unsigned long long no = ~__ballot(ok);          // (lanes n .. 63 are never ok, and n <= 63)
-        if (lane == 0) s_stand = (int)__builtin_ctzll(no);
-    }
-    __syncthreads();
-    const int stand = s_stand;
-    const bool refused = stand < n, has_q = refused && a.draft_logits;
-    const int qtoken = refused && !a.draft_logits ? a.draft[(size_t)b * D + stand] : -1;
-    const Row tr = row_of(a.logits + ((size_t)b * (D + 1) + stand) * V, V);
-    const Row dr = has_q ? row_of(a.draft_logits + ((size_t)b * D + stand) * V, V) : tr;
-    const Mass pm = s_mass[stand], qm = has_q ? s_mass[n + 1 + stand] : Mass{0.0, 0.0};
-    const double pinv = pm.sum > 0.0 ? 1.0 / pm.sum : 0.0, qinv = qm.sum > 0.0 ? 1.0 / qm.sum : 0.0;
-
-    Values v;
-    stop_values(a, tr, dr, has_q, qtoken, pm, pinv, qm, qinv, c, chunk * kDrawGroups + 2 * tid, v);
+    Values<J> v;
+    stop_values<J>(a, tr, dr, st, c, (chunk * kThreads + tid) * J, v);
     double rest = 0.0, all = 0.0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8 * J; ++e) {
         rest += v.rest[e];
         all += v.all[e];
     }
@@ -428,32 +503,30 @@ __global__ __launch_bounds__(kThreads) void verify_full_kernel(VerifyArgs a, int
     }
     __syncthreads();
     Part* mine = parts + (size_t)b * chunks;
-    if (tid == 0) {
-        put(&mine[chunk].rest, s_wave[0][0] + s_wave[0][1] + s_wave[0][2] + s_wave[0][3]);
-        put(&mine[chunk].all, s_wave[1][0] + s_wave[1][1] + s_wave[1][2] + s_wave[1][3]);
-    }
+    if (tid < 2) put(tid ? &mine[chunk].all : &mine[chunk].rest, s_wave[tid][0] + s_wave[tid][1] + s_wave[tid][2] + s_wave[tid][3]);
     if (!arrive_last(cnt + (size_t)b * kCtrWords, chunks, tid, &s_prev)) return;
 
     // the chunk where the running sum crosses u_D times the total
     if (wave == 0) {
         const int per = (chunks + 63) >> 6;
-        double rs = 0.0, as = 0.0;
+        double rs = 0.0, as = 0.0, ru = a.u[(size_t)b * (D + 1) + D];
         for (int i = lane * per; i < (lane + 1) * per && i < chunks; ++i) {
             rs += get(&mine[i].rest);
             as += get(&mine[i].all);
         }
-        const bool use_rest = wave_sum(rs) > 0.0;
+        const bool use_rest = __ballot(rs > 0.0) != 0;
         const double own = use_rest ? rs : as;
         const double run = wave_scan(own, lane), total = lane_value(run, 63);
-        const double x = (double)a.u[(size_t)b * (D + 1) + D] * total;
+        const double x = ru * total;
         const unsigned long long over = __ballot(run > x), any = __ballot(own > 0.0);
         const int l = over ? (int)__builtin_ctzll(over) : any ? 63 - (int)__builtin_clzll(any) : -1;
         if (l < 0) {
             if (lane == 0) s_chunk = -1;
         } else if (lane == l) {
             double before = run - own;
-            int at = -1;
-            for (int i = lane * per; i < (lane + 1) * per && i < chunks; ++i) {
+            int at = per == 1 ? lane : -1;
+            s_before = before;
+            for (int i = lane * per; per > 1 && i < (lane + 1) * per && i < chunks; ++i) {
                 const double w = use_rest ? get(&mine[i].rest) : get(&mine[i].all);
                 if (w > 0.0) {
                     at = i;
@@ -464,60 +537,54 @@ __global__ __launch_bounds__(kThreads) void verify_full_kernel(VerifyArgs a, int
             }
             s_chunk = at;
             s_x = x;
-            s_stand = use_rest ? 1 : 0;
+            s_rest = use_rest;
         }
     }
-    if (tid == 0) s_token = -1;
     __syncthreads();
     const int hit = s_chunk;
-    if (hit >= 0) {
-        const bool use_rest = s_stand != 0;
-        const double x = s_x;
-        stop_values(a, tr, dr, has_q, qtoken, pm, pinv, qm, qinv, c, hit * kDrawGroups + 2 * tid, v);
-        double own = 0.0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            if (!use_rest) v.rest[e] = v.all[e];
-            own += v.rest[e];
-        }
-        const double run = wave_scan(own, lane);
-        __syncthreads();
-        if (lane == 63) s_wave[0][wave] = run;
-        __syncthreads();
-        double before = s_before;
-        for (int w = 0; w < wave; ++w) before += s_wave[0][w];
-        before += run - own;
-        // the first value whose running sum exceeds x; where rounding leaves
-        // none, the chunk's last value above zero
-        int first = 0x7FFFFFFF, last = -1;
-        const int i0 = 8 * (hit * kDrawGroups + 2 * tid) - tr.off;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            before += v.rest[e];
-            if (v.rest[e] > 0.0) {
-                if (before > x && first == 0x7FFFFFFF) first = i0 + e;
-                last = i0 + e;
-            }
-        }
-#pragma unroll
-        for (int s = 1; s < 64; s *= 2) {
-            first = min(first, __shfl_xor(first, s));
-            last = max(last, __shfl_xor(last, s));
-        }
-        __shared__ int s_first[4], s_last[4];
-        if (lane == 0) {
-            s_first[wave] = first;
-            s_last[wave] = last;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            const int f = min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3]));
-            const int l = max(max(s_last[0], s_last[1]), max(s_last[2], s_last[3]));
-            s_token = f != 0x7FFFFFFF ? f : l;
-        }
-        __syncthreads();
+    int32_t* token = a.token + (size_t)b * (D + 1) + st.stand;
+    if (hit < 0) {
+        if (tid == 0) *token = -1;
+        return;
     }
-    write_tokens(a, b, stand, s_token, tid);
+    if (hit != chunk) stop_values<J>(a, tr, dr, st, c, (hit * kThreads + tid) * J, v);
+    double own = 0.0;
+    const bool use_rest = s_rest != 0;
+#pragma unroll
+    for (int e = 0; e < 8 * J; ++e) {
+        if (!use_rest) v.rest[e] = v.all[e];
+        own += v.rest[e];
+    }
+    const double run = wave_scan(own, lane), x = s_x;
+    if (lane == 63) s_wave[0][wave] = run;
+    __syncthreads();
+    double before = s_before;
+    for (int w = 0; w < wave; ++w) before += s_wave[0][w];
+    before += run - own;
+    // the first value whose running sum exceeds x; where rounding leaves none,
+    // the chunk's last value above zero
+    int first = 0x7FFFFFFF, last = -1;
+    const int i0 = 8 * (hit * kThreads + tid) * J - tr.off;
+#pragma unroll
+    for (int e = 0; e < 8 * J; ++e) {
+        before += v.rest[e];
+        if (v.rest[e] > 0.0) {
+            if (before > x && first == 0x7FFFFFFF) first = i0 + e;
+            last = i0 + e;
+        }
+    }
+    const unsigned long long have = __ballot(first != 0x7FFFFFFF), some = __ballot(last >= 0);
+    const int f = __shfl(first, have ? (int)__builtin_ctzll(have) : 0), g = __shfl(last, some ? 63 - (int)__builtin_clzll(some) : 0);
+    if (lane == 0) {
+        s_first[wave] = f;
+        s_last[wave] = g;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const int lo = min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3]));
+        const int hi = max(max(s_last[0], s_last[1]), max(s_last[2], s_last[3]));
+        *token = lo != 0x7FFFFFFF ? lo : hi;
+    }
 }
 
 double log2e_over(float temperature) { return 1.4426950408889634 / (double)temperature; }
@@ -525,8 +592,8 @@ constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// The workspace's first kWsCounterBytes stay as they are (other calls' arrival
-// counters); everything after them is scratch that needs no clearing.
+// The workspace's first kWsCounterBytes are arrival counters (zero before and
+// after every call), everything after them is scratch.
 size_t verify_topk_ws_bytes(int B, int D, int V, int top_k) {
     if (V <= kDirectVocab) return 0;
     const size_t nb = (V + kSplitBlock - 1) / kSplitBlock;
@@ -550,27 +617,74 @@ hipError_t launch_verify_topk(const VerifyArgs& a, void* ws, hipStream_t s) {
     return launch_kernel(verify_topk_kernel<32>, grid, block, 0, s, a, nc, c, in);     // nc <= 30 * 64
 }
 
-// Sequence counters (cleared by the first launch), the rows' masses by chunk,
-// the sequences' partial sums by chunk.
+namespace {
+struct FullPlan {
+    int rows, mass_j, draw_j;
+    size_t mass_chunks, draw_chunks, stop_bytes, mass_bytes;
+};
+// Workgroups of a chunk of 256 J groups: fewer groups where the whole launch is
+// under two workgroups per CU (V = 16385, one sequence: 8 against 32
+// exponentials per thread).
+FullPlan full_plan(int B, int D, int V, bool drafts, bool aligned) {
+    FullPlan p;
+    const size_t g = row_groups(V, aligned);
+    const int b = B < kSequences ? B : kSequences;
+    auto chunks = [&](int j) { return (g + (size_t)kThreads * j - 1) / ((size_t)kThreads * j); };
+    p.rows = D + 1 + (drafts ? D : 0);
+    p.mass_j = (size_t)b * p.rows * chunks(kMassJ) < 512 ? 1 : kMassJ;
+    p.draw_j = (size_t)b * chunks(kDrawJ) < 512 ? 1 : kDrawJ;
+    p.mass_chunks = chunks(p.mass_j);
+    p.draw_chunks = chunks(p.draw_j);
+    p.stop_bytes = up256((size_t)b * sizeof(Stop));
+    p.mass_bytes = up256((size_t)b * p.rows * p.mass_chunks * sizeof(Mass));
+    return p;
+}
+}  // namespace
+
+// Stops, masses by chunk, partial sums by chunk.
 size_t verify_full_ws_bytes(int B, int D, int V) {
-    const size_t rows = (size_t)B * (2 * D + 1), g = row_groups_most(V);
-    const size_t mc = (g + kMassGroups - 1) / kMassGroups, dc = (g + kDrawGroups - 1) / kDrawGroups;
-    return kWsCounterBytes + up256((size_t)B * kCtrStride) + up256(rows * mc * sizeof(Mass)) + (size_t)B * dc * sizeof(Part);
+    const int b = B < kSequences ? B : kSequences;
+    size_t most = 0;
+    for (int k = 0; k < 4; ++k) {
+        const FullPlan x = full_plan(B, D, V, k & 1, k & 2);
+        const size_t n = x.stop_bytes + x.mass_bytes + (size_t)b * x.draw_chunks * sizeof(Part);
+        most = n > most ? n : most;
+    }
+    return kWsCounterBytes + most;
 }
 
-hipError_t launch_verify_full(const VerifyArgs& a, void* ws, hipStream_t s) {
-    const size_t rows = (size_t)a.B * (2 * a.D + 1), g = row_groups_most(a.V);
-    const int mc = (int)((g + kMassGroups - 1) / kMassGroups), dc = (int)((g + kDrawGroups - 1) / kDrawGroups);
-    uint8_t* p = static_cast<uint8_t*>(ws) + kWsCounterBytes;
-    unsigned* cnt = reinterpret_cast<unsigned*>(p);
-    Mass* mass = reinterpret_cast<Mass*>(p + up256((size_t)a.B * kCtrStride));
-    Part* parts = reinterpret_cast<Part*>(reinterpret_cast<uint8_t*>(mass) + up256(rows * mc * sizeof(Mass)));
-    const double c = log2e_over(a.temperature);
-    const size_t run = a.draft_logits ? rows : (size_t)a.B * (a.D + 1);
-    hipError_t e = launch_kernel(row_mass_kernel, dim3((unsigned)(run * mc)), dim3(kThreads), 0, s, a, mc, c, mass, cnt);
-    if (e != hipSuccess) return e;
-    return launch_kernel(verify_full_kernel, dim3((unsigned)(a.B * dc)), dim3(kThreads), 0, s, a, mc, dc, c, (const Mass*)mass, cnt,
-                         parts);
+hipError_t launch_verify_full(const VerifyArgs& args, void* ws, hipStream_t s) {
+    const bool aligned =
+        args.V % 8 == 0 && ((reinterpret_cast<uintptr_t>(args.logits) | reinterpret_cast<uintptr_t>(args.draft_logits)) & 15) == 0;
+    const FullPlan p = full_plan(args.B, args.D, args.V, args.draft_logits != nullptr, aligned);
+    unsigned* cnt = static_cast<unsigned*>(ws);
+    Stop* stop = reinterpret_cast<Stop*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
+    Mass* mass = reinterpret_cast<Mass*>(reinterpret_cast<uint8_t*>(stop) + p.stop_bytes);
+    Part* parts = reinterpret_cast<Part*>(reinterpret_cast<uint8_t*>(mass) + p.mass_bytes);
+    const double c = log2e_over(args.temperature);
+    for (int b0 = 0; b0 < args.B; b0 += kSequences) {
+        VerifyArgs a = args;
+        const size_t t0 = (size_t)b0 * (a.D + 1), d0 = (size_t)b0 * a.D;
+        a.B = args.B - b0 < kSequences ? args.B - b0 : kSequences;
+        a.logits += t0 * a.V;
+        if (a.draft_logits) a.draft_logits += d0 * a.V;
+        a.draft += d0;
+        if (a.n_draft) a.n_draft += b0;
+        a.u += t0;
+        a.token += t0;
+        a.count += b0;
+        if (a.accept_prob) a.accept_prob += d0;
+        const dim3 first((unsigned)((size_t)a.B * p.rows * p.mass_chunks)), second((unsigned)((size_t)a.B * p.draw_chunks)), block(kThreads);
+        const int mc = (int)p.mass_chunks, dc = (int)p.draw_chunks;
+        hipError_t e = p.mass_j == 1 ? launch_kernel(row_mass_kernel<1>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop)
+                                     : launch_kernel(row_mass_kernel<kMassJ>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop);
+        if (e != hipSuccess) return e;
+        const Stop* st = stop;
+        e = p.draw_j == 1 ? launch_kernel(stop_draw_kernel<1>, second, block, 0, s, a, dc, c, st, cnt, parts)
+                          : launch_kernel(stop_draw_kernel<kDrawJ>, second, block, 0, s, a, dc, c, st, cnt, parts);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace q4

@@ -484,8 +484,10 @@ int fp8b128_workspace_bytes(const fp8b128_task* tasks, int count, int M, size_t*
  *
  * 1 <= D <= 63, B (D + 1) <= 65536; temperature finite and > 0.  Alignment:
  * logits 2 bytes, everything else 4.  workspace: at least
- * q4_verify_*_workspace_bytes (where that is not 0), 256-byte aligned; its
- * first 64 KiB stay as they are, the rest is scratch that needs no clearing.
+ * q4_verify_*_workspace_bytes (where that is not 0), 256-byte aligned,
+ * zero-filled before its first use; its first 64 KiB are arrival counters that
+ * every call leaves at zero, the rest is scratch, so it can be shared with the
+ * library's other calls that take a workspace of this kind.
  * Calls that use one workspace must not overlap in time.  Returns
  * Q4_EINVAL_PTR (no workspace where one is needed too), Q4_EINVAL_SHAPE,
  * Q4_EALIGN, Q4_ESCRATCH (workspace too small) or Q4_EALIAS before anything is

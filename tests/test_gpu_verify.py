@@ -145,7 +145,7 @@ def want_full(lg, d, u, dl, n, T):
 
 
 FULL = [(1, 1, 1, 0.8), (1, 1, 7, 1.0), (2, 63, 33, 0.8), (1, 4, 2049, 0.8), (5, 3, 4095, 1.3), (3, 4, 8193, 0.5), (4, 2, 16385, 0.8),
-        (2, 7, 50000, 1.0), (3, 1, 131072, 1.0), (1, 2, 200001, 0.8), (1, 1, 1 << 20, 1.0)]
+        (2, 7, 50000, 1.0), (3, 1, 131072, 1.0), (1, 2, 200001, 0.8), (1, 1, 1 << 20, 1.0), (520, 1, 40, 0.8), (100, 4, 2056, 0.8)]
 
 
 @pytest.mark.parametrize("B,D,V,T", FULL)
@@ -213,7 +213,7 @@ def test_stream_and_graph(q4, form):
         sets.append([gpu(t) for t in (lg, dl, u, n, qi, qp, d)])
     cur = [t.clone() for t in sets[0]]
     size = q4.verify_topk_workspace_bytes(B, D, V, k) if form == "topk" else q4.verify_full_workspace_bytes(B, D, V)
-    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
 
     def step():
         lg, dl, u, n, qi, qp, d = cur
