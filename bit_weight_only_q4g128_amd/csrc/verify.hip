@@ -239,8 +239,7 @@ __global__ __launch_bounds__(kTopkWaves * 64) void verify_topk_kernel(VerifyArgs
 // of 8 logits that touch it; the first and the last, where the row ends inside
 // them, value by value.
 // ---------------------------------------------------------------------------
-constexpr int kMassJ = 4;      // groups of 8 logits per thread of the first launch (1 where the workgroups are few)
-constexpr int kDrawJ = 2;      // of the second, adjacent ones (likewise)
+constexpr int kDrawJ = 2;      // adjacent groups of 8 logits per thread of the second launch (1 where the workgroups are few)
 constexpr int kSequences = (int)(kWsCounterBytes / kCtrStride);      // sequences of one pair of launches
 
 struct Row {
@@ -274,10 +273,13 @@ __device__ __forceinline__ void load_groups(const Row& r, int V, const int (&g)[
     for (int j = 0; j < NJ; ++j) {
         if (g[j] >= lo && g[j] < hi) continue;
         const int i0 = 8 * g[j] - r.off;
+        v[j] = u32x4{kNone, kNone, kNone, kNone};
+        if (i0 <= -8 || i0 >= V) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 2 * e;
-            const uint32_t a = i >= 0 && i < V ? r.p[i] : 0xFF80u, b = i + 1 >= 0 && i + 1 < V ? r.p[i + 1] : 0xFF80u;
+            const int i = i0 + 2 * e, ia = i < 0 ? 0 : i < V ? i : V - 1, ib = i + 1 < 0 ? 0 : i + 1 < V ? i + 1 : V - 1;
+            const uint32_t ra = r.p[ia], rb = r.p[ib];      // (inside the row, so that all are in flight together)
+            const uint32_t a = ia == i ? ra : 0xFF80u, b = ib == i + 1 ? rb : 0xFF80u;
             v[j][e] = a | (b << 16);
         }
     }
@@ -383,52 +385,180 @@ __device__ __forceinline__ void accept(const VerifyArgs& a, int b, int n, int ch
 
 // Block (sequence, row, chunk); a sequence's rows are the target's D + 1, then
 // the draft's D.
-template <int J>
-__global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int rows, int chunks, double c, Mass* mass, unsigned* cnt,
-                                                            Stop* stop) {
+struct MassBlock {
+    int b, n, rest, chunk;      // sequence, its drafted tokens, row and chunk in one, chunk
+    Row row;
+    bool live;                  // a drafted token leads here
+};
+__device__ __forceinline__ MassBlock mass_block(const VerifyArgs& a, int rows, int chunks) {
+    MassBlock m;
+    m.b = blockIdx.x / (rows * chunks);
+    m.rest = blockIdx.x - m.b * rows * chunks;
+    const int i = m.rest / chunks;
+    m.chunk = m.rest - i * chunks;
+    m.n = drafted(a, m.b);
+    const bool target = i <= a.D;
+    m.live = target ? i <= m.n : i - a.D - 1 < m.n;
+    m.row = row_of(target ? a.logits + ((size_t)m.b * (a.D + 1) + i) * a.V : a.draft_logits + ((size_t)m.b * a.D + (i - a.D - 1)) * a.V,
+                   a.V);
+    return m;
+}
+// The workgroup's mass from its threads' (top, sum); the workgroup that ends
+// the sequence's last chunk accepts.
+__device__ __forceinline__ void mass_end(const VerifyArgs& a, const MassBlock& mb, float top, double sum, int rows, int chunks, double c,
+                                         Mass* mass, unsigned* cnt, Stop* stop) {
     __shared__ float s_top[4];
     __shared__ double s_sum[4];
     __shared__ unsigned s_prev;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int b = blockIdx.x / (rows * chunks), rest = blockIdx.x - b * rows * chunks;
-    const int i = rest / chunks, chunk = rest - i * chunks;
-    const int n = drafted(a, b);
-    const bool target = i <= a.D;
-    if (target ? i > n : i - a.D - 1 >= n) return;                     // no drafted token leads here
-    const Row r = row_of(target ? a.logits + ((size_t)b * (a.D + 1) + i) * a.V : a.draft_logits + ((size_t)b * a.D + (i - a.D - 1)) * a.V,
-                         a.V);
+    float m = top;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
+    if (lane == 0) s_top[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+    sum = wave_sum(sum * exp2_64(((double)top - (double)m) * c));
+    if (lane == 0) s_sum[wave] = sum;
+    __syncthreads();
+    Mass* mine = mass + (size_t)mb.b * rows * chunks;
+    if (tid == 0) {
+        put(&mine[mb.rest].sum, s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
+        put(&mine[mb.rest].top, (double)m);
+    }
+    const int active = mb.n + 1 + (a.draft_logits ? mb.n : 0);
+    if (!arrive_last(cnt + (size_t)mb.b * kCtrWords, active * chunks, tid, &s_prev)) return;
+    accept(a, mb.b, mb.n, chunks, c, mine, stop + mb.b, tid);
+}
+
+// Short rows: J groups per thread, one exponential per logit.
+template <int J>
+__global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int rows, int chunks, double c, Mass* mass, unsigned* cnt,
+                                                            Stop* stop) {
+    const MassBlock mb = mass_block(a, rows, chunks);
+    if (!mb.live) return;
     u32x4 v[J];
     int at[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) at[j] = (chunk * J + j) * kThreads + tid;
-    load_groups<J>(r, a.V, at, v);
+    for (int j = 0; j < J; ++j) at[j] = (mb.chunk * J + j) * kThreads + (int)threadIdx.x;
+    load_groups<J>(mb.row, a.V, at, v);
     float top = -__builtin_huge_valf();
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, half_of(v[j], e));
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-    if (lane == 0) s_top[wave] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
     double sum = 0.0;
     const double base = -(double)top * c;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += exp2_raw(__builtin_fma((double)half_of(v[j], e), c, base));
-    sum = wave_sum(sum);
-    if (lane == 0) s_sum[wave] = sum;
+    mass_end(a, mb, top, sum, rows, chunks, c, mass, cnt, stop);
+}
+
+// Long rows of many sequences: a row's part holds few distinct bf16 values, so
+// they are counted in LDS, one bin per value of 2^-12 <= |z| < 2^6, and each bin
+// takes one exponential (18 per thread instead of up to 256; counts are exact,
+// and the sum does not depend on the order of the additions to them).  Other
+// values, rare in logits, are added one by one; -inf and NaN not at all.
+// An exponential per logit is bound by the fp64 arithmetic: 32 sequences with 7
+// drafted tokens and V = 131072, both launches, 67 us against 53 us, 128 with 4
+// and V = 32768 54 against 49.  It stays the better one below that (128 with 4,
+// V = 8192: 23 against 27 us), and for rows of other logits: nearly all of them
+// the type's lowest value or zero 66 against 90 us, all the same value 65
+// against 190 (the bin's additions wait for each other).
+constexpr int kHistJ = 32;                              // most groups per thread
+constexpr int kHistStep = 4;                            // of them at a time
+constexpr uint32_t kBinLow = 0x3980, kBins = 18 * 128;  // bits of 2^-12; bins of one sign
+constexpr uint32_t kBinSign = 4096;                     // first bin of the negative values
+constexpr int kBinWords = (int)(kBinSign + kBins + 64); // (behind either sign's: the other values, a bin per lane, not read)
+
+__global__ __launch_bounds__(kThreads) void row_mass_hist_kernel(VerifyArgs a, int rows, int chunks, int steps, double c, Mass* mass,
+                                                                 unsigned* cnt, Stop* stop) {
+    __shared__ __attribute__((aligned(16))) uint32_t bins[(kBinWords + 3) & ~3];
+    const MassBlock mb = mass_block(a, rows, chunks);
+    if (!mb.live) return;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < (kBinWords + 3) / 4; i += kThreads) reinterpret_cast<u32x4*>(bins)[i] = u32x4{0, 0, 0, 0};
+    constexpr int J = kHistStep;
+    u32x4 v[J];
+    auto load = [&](int s) {
+        int at[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) at[j] = ((mb.chunk * steps + s) * J + j) * kThreads + tid;
+        load_groups<J>(mb.row, a.V, at, v);
+    };
+    load(0);
     __syncthreads();
-    Mass* mine = mass + (size_t)b * rows * chunks;
-    if (tid == 0) {
-        put(&mine[rest].sum, s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
-        put(&mine[rest].top, (double)top);
+    const unsigned short most = (unsigned short)(kBins + (tid & 63));
+    float top = -__builtin_huge_valf();
+    double sum = 0.0;
+    const int inside = ((mb.row.off + a.V + 7) / 8 - mb.chunk * steps * J * kThreads + J * kThreads - 1) / (J * kThreads);
+    const int end = inside < steps ? inside : steps;
+#pragma unroll 1
+    for (int s = 0; s < end; ++s) {
+        // bin numbers in pairs of 16 bits: |z|'s bits less kBinLow (smaller ones
+        // wrap), at most kBins + lane, plus the sign's 4096
+        uint32_t t[J][4];
+        bool other = false;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+                const uint32_t pair = v[j][e];      // (a bit_cast of the vector's element itself reads element 0)
+                const u16x2 b = __builtin_bit_cast(u16x2, pair);
+                u16x2 m = (u16x2)(b & (unsigned short)0x7FFF) - (unsigned short)kBinLow;
+                m = __builtin_elementwise_min(m, u16x2{most, most});
+                other = other || m.x >= kBins || m.y >= kBins;
+                m += (u16x2)((b >> 15) << 12);
+                t[j][e] = __builtin_bit_cast(uint32_t, m);
+            }
+        if (__any(other)) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float z = half_of(v[j], e);
+                    const bool mine = ((t[j][e >> 1] >> (e & 1 ? 16 : 0)) & (kBinSign - 1)) >= kBins && z > -__builtin_huge_valf();
+                    if (!__any(mine)) continue;
+                    // many of them are alike: zeros, masks of the type's lowest value
+                    double r = 1.0;
+                    if (__any(mine && z != top)) r = z == top ? 1.0 : exp2_64(-fabs((double)z - (double)top) * c);
+                    const double more = z > top ? sum * r + 1.0 : sum + r;
+                    sum = mine ? more : sum;
+                    top = mine ? fmaxf(top, z) : top;
+                }
+        }
+        if (s + 1 < end) load(s + 1);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                atomicAdd(&bins[t[j][e] & 0xFFFFu], 1u);
+                atomicAdd(&bins[t[j][e] >> 16], 1u);
+            }
     }
-    const int active = n + 1 + (a.draft_logits ? n : 0);
-    if (!arrive_last(cnt + (size_t)b * kCtrWords, active * chunks, tid, &s_prev)) return;
-    accept(a, b, n, chunks, c, mine, stop + b, tid);
+    __syncthreads();
+    // one exponential per bin in use
+    constexpr int kPer = (int)(2 * kBins) / kThreads;
+    static_assert(2 * kBins % kThreads == 0, "bins");
+    float m = top;
+    uint32_t n[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t i = k * kThreads + tid, sign = i >= kBins, bin = i - (sign ? kBins : 0u);
+        n[k] = bins[bin + sign * kBinSign];
+        const float z = __builtin_bit_cast(float, (bin + kBinLow + (sign << 15)) << 16);
+        m = n[k] ? fmaxf(m, z) : m;
+    }
+    sum *= exp2_64(((double)top - (double)m) * c);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t i = k * kThreads + tid, sign = i >= kBins, bin = i - (sign ? kBins : 0u);
+        const float z = __builtin_bit_cast(float, (bin + kBinLow + (sign << 15)) << 16);
+        if (n[k]) sum += (double)n[k] * exp2_64(((double)z - (double)m) * c);
+    }
+    mass_end(a, mb, m, sum, rows, chunks, c, mass, cnt, stop);
 }
 
 struct Part {
@@ -619,21 +749,29 @@ hipError_t launch_verify_topk(const VerifyArgs& a, void* ws, hipStream_t s) {
 
 namespace {
 struct FullPlan {
-    int rows, mass_j, draw_j;
+    int rows, mass_steps, mass_j, draw_j;     // steps of the counting kernel (0: the other, groups per thread)
     size_t mass_chunks, draw_chunks, stop_bytes, mass_bytes;
 };
-// Workgroups of a chunk of 256 J groups: fewer groups where the whole launch is
-// under two workgroups per CU (V = 16385, one sequence: 8 against 32
-// exponentials per thread).
+// Chunks of 256 J groups: as many groups per thread as leave the launch two
+// workgroups per CU.  A batch of 32 with 131072 logits and 7 drafted tokens runs
+// on parts of 8 steps of the counting kernel, one sequence with 16385 on one
+// group per thread.
 FullPlan full_plan(int B, int D, int V, bool drafts, bool aligned) {
     FullPlan p;
     const size_t g = row_groups(V, aligned);
     const int b = B < kSequences ? B : kSequences;
     auto chunks = [&](int j) { return (g + (size_t)kThreads * j - 1) / ((size_t)kThreads * j); };
     p.rows = D + 1 + (drafts ? D : 0);
-    p.mass_j = (size_t)b * p.rows * chunks(kMassJ) < 512 ? 1 : kMassJ;
+    const size_t wanted = 512 / (size_t)b / p.rows + 1;
+    p.mass_steps = 0;
+    p.mass_j = chunks(4) >= wanted ? 4 : 1;
     p.draw_j = (size_t)b * chunks(kDrawJ) < 512 ? 1 : kDrawJ;
     p.mass_chunks = chunks(p.mass_j);
+    if (chunks(kHistJ) >= wanted && g >= 16 * kThreads) {       // both sides measured at row_mass_hist_kernel
+        p.mass_chunks = chunks(kHistJ);
+        p.mass_steps = (int)((g + kThreads * kHistStep * p.mass_chunks - 1) / (kThreads * kHistStep * p.mass_chunks));
+        p.mass_chunks = chunks(p.mass_steps * kHistStep);
+    }
     p.draw_chunks = chunks(p.draw_j);
     p.stop_bytes = up256((size_t)b * sizeof(Stop));
     p.mass_bytes = up256((size_t)b * p.rows * p.mass_chunks * sizeof(Mass));
@@ -676,8 +814,9 @@ hipError_t launch_verify_full(const VerifyArgs& args, void* ws, hipStream_t s) {
         if (a.accept_prob) a.accept_prob += d0;
         const dim3 first((unsigned)((size_t)a.B * p.rows * p.mass_chunks)), second((unsigned)((size_t)a.B * p.draw_chunks)), block(kThreads);
         const int mc = (int)p.mass_chunks, dc = (int)p.draw_chunks;
-        hipError_t e = p.mass_j == 1 ? launch_kernel(row_mass_kernel<1>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop)
-                                     : launch_kernel(row_mass_kernel<kMassJ>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop);
+        hipError_t e = p.mass_steps    ? launch_kernel(row_mass_hist_kernel, first, block, 0, s, a, p.rows, mc, p.mass_steps, c, mass, cnt, stop)
+                       : p.mass_j == 4 ? launch_kernel(row_mass_kernel<4>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop)
+                                       : launch_kernel(row_mass_kernel<1>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop);
         if (e != hipSuccess) return e;
         const Stop* st = stop;
         e = p.draw_j == 1 ? launch_kernel(stop_draw_kernel<1>, second, block, 0, s, a, dc, c, st, cnt, parts)

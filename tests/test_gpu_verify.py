@@ -188,6 +188,39 @@ def test_full_odd_inputs(q4):
     check(run_full(q4, lg, d, u, dl, n, T), want_full(lg, d, u, dl, n, T))
 
 
+@pytest.mark.parametrize("V", [32768, 33001, 40003, 70001])
+def test_full_long_rows_of_many_sequences(q4, V):
+    """Rows whose logits are counted by value: ordinary ones, and values outside
+    the counted range (zeros, tiny and large ones, masks of the lowest value,
+    -inf, NaN), rows of one value, rows without a distribution."""
+    B, D, T = 80, 3, 0.8
+    print(f"verify_full B={B} D={D} V={V}", flush=True)
+    lg, dl, u, n, g = inputs(B, D, V, 11)
+    d = drawn_of(dl, T, g)
+    low = float(torch.finfo(torch.bfloat16).min)
+    for k, value in enumerate((0.0, -0.0, 1e-6, -2e-5, low, float("-inf"), float("nan"))):
+        at = torch.rand(V, generator=g) < (0.5 if k % 2 else 0.98)
+        lg[k, :, at] = value
+        dl[k, :, at] = value
+    lg[7], dl[7] = low, low
+    lg[8], dl[8] = 0.0, 0.0
+    lg[9], dl[9] = 1.5, 1.5
+    lg[10], dl[10] = -0.0, 3e-5
+    lg[11] *= 60
+    lg[12], dl[12] = lg[12] * 1e-4, dl[12] * 1e-4
+    lg[13] += 60
+    lg[14] -= 100
+    lg[15, 0] = float("-inf")
+    lg[16, 1] = float("nan")
+    lg[17, 0, V - 1] = float("inf")
+    dl[18, 0] = float("-inf")
+    lg[19, :, V - 1] = 300.0
+    lg[20], dl[20] = low, low
+    lg[20, :, 7] = -1e38
+    n[:24] = D
+    check(run_full(q4, lg, d, u, dl, n, T), want_full(lg, d, u, dl, n, T))
+
+
 def test_dirty_shared_workspace(q4):
     """One workspace for both forms and for products, its scratch full of
     rubbish, its first 64 KiB left as they are."""
