@@ -60,20 +60,46 @@ __device__ __forceinline__ double exp2_64(double y) {
     return y > -1000.0 ? v : 0.0;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) v += __shfl_xor(v, s);
+// Inclusive prefix sum over the 64 lanes, and the sum (lane 63's), by DPP
+// moves: a shuffle through LDS costs several times their latency, and the
+// verification of one sequence is little but such chains.
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ double dpp64(double v) {
+    uint2 w = __builtin_bit_cast(uint2, v);
+    w.x = (uint32_t)dpp_i<CTRL, ROW_MASK>((int)w.x);
+    w.y = (uint32_t)dpp_i<CTRL, ROW_MASK>((int)w.y);
+    return __builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ double wave_scan(double v) {
+    v += dpp64<0x111>(v);        // row_shr:1
+    v += dpp64<0x112>(v);        // row_shr:2
+    v += dpp64<0x114>(v);        // row_shr:4
+    v += dpp64<0x118>(v);        // row_shr:8
+    v += dpp64<0x142, 0xA>(v);   // row_bcast:15 into rows 1, 3
+    v += dpp64<0x143, 0xC>(v);   // row_bcast:31 into rows 2, 3
     return v;
 }
-__device__ __forceinline__ double wave_scan(double v, int lane) {      // inclusive
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-        const double o = __shfl_up(v, s);
-        v += lane >= s ? o : 0.0;
-    }
-    return v;
+__device__ __forceinline__ double lane_value(double v, int lane) {      // lane: the same in every lane
+    uint2 w = __builtin_bit_cast(uint2, v);
+    w.x = (uint32_t)__builtin_amdgcn_readlane((int)w.x, lane);
+    w.y = (uint32_t)__builtin_amdgcn_readlane((int)w.y, lane);
+    return __builtin_bit_cast(double, w);
 }
-__device__ __forceinline__ double lane_value(double v, int lane) { return __shfl(v, lane); }
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ float dpp_max(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, CTRL, ROW_MASK, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = dpp_max<0x111>(v);
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) { return lane_value(wave_scan(v), 63); }
 
 // Values that another workgroup of the same launch reads: device-coherent
 // accesses, ordered by arrive_last().
@@ -92,48 +118,45 @@ __device__ __forceinline__ float accept_ratio(double p, double q) {
     return q > 0.0 ? (p < q ? (float)(p / q) : 1.0f) : (p > 0.0 ? 1.0f : 0.0f);
 }
 
-// The outputs of sequence b: the tokens that stand, the new one, -1 behind it.
-__device__ __forceinline__ void write_tokens(const VerifyArgs& a, int b, int stand, int token, int tid) {
-    if (tid <= a.D) a.token[(size_t)b * (a.D + 1) + tid] = tid < stand ? a.draft[(size_t)b * a.D + tid] : tid == stand ? token : -1;
-    if (tid == 0) a.count[b] = stand;
-}
-
 // ---------------------------------------------------------------------------
 // top-k form.  Rows of at most kDirectVocab logits: one launch, a workgroup
 // per sequence, a wave per row.  Longer rows: a first launch takes the top k
-// of every block of 1024 logits, and the waves of the second merge a row's
+// of every block of 1024 or 4096, and the waves of the second merge a row's
 // candidates.  Nothing is handed over inside a launch.
 // ---------------------------------------------------------------------------
-constexpr int kTopkWaves = 8;
-constexpr int kDirectE = 40;                        // logits per lane of the one-launch form
-constexpr int kDirectVocab = 64 * kDirectE;
+constexpr int kRowsAtOnce = 8;                      // of a workgroup of the last launch
+constexpr int kPairE = 20;                          // entries per lane of two waves that share a row
+constexpr int kDirectVocab = 2 * 64 * kPairE;
+constexpr int kBlockE = 4, kLongBlockE = 16;        // logits per thread of a block of the first launch
 
 // NaN counts as -inf
 __device__ __forceinline__ uint32_t entry_of(uint32_t bits, int col) {
     return topk_entry((bits & 0x7FFFu) > 0x7F80u ? 0xFF80u : bits, col);
 }
 
+template <int E>
 __global__ __launch_bounds__(kThreads) void block_topk_kernel(VerifyArgs a, int nb, uint32_t* cand) {
+    constexpr int kLogits = kThreads * E;
     __shared__ uint32_t lists[4 * 64];
-    __shared__ uint32_t scratch[4 * 64 * 4];
+    __shared__ uint32_t scratch[4 * 64 * E];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row = blockIdx.x / nb, j = blockIdx.x - row * nb;
     const int b = row / (a.D + 1), r = row - b * (a.D + 1);
     if (r > drafted(a, b)) return;                        // no drafted token leads here
     const uint16_t* lg = a.logits + (size_t)row * a.V;
-    uint32_t v[4];
+    uint32_t v[E];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int col = j * kSplitBlock + tid + 256 * i;
+    for (int i = 0; i < E; ++i) {
+        const int col = j * kLogits + tid + 256 * i;
         v[i] = lg[col < a.V ? col : 0];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int col = j * kSplitBlock + tid + 256 * i;
+    for (int i = 0; i < E; ++i) {
+        const int col = j * kLogits + tid + 256 * i;
         v[i] = col < a.V ? entry_of(v[i], col) : 0u;
     }
-    const uint32_t top = wg_topk<4>(v, a.top_k, lists, scratch, wave, lane);
+    const uint32_t top = wg_topk<E>(v, a.top_k, lists, scratch, wave, lane);
     if (wave == 0 && lane < a.top_k) cand[((size_t)row * nb + j) * a.top_k + lane] = top;
 }
 
@@ -147,86 +170,108 @@ __device__ __forceinline__ double topk_prob64(uint32_t entry, int k, double c, i
     return s > 0.0 ? e / s : 0.0;
 }
 
-// One workgroup per sequence.  cand null: rows are read as they are.
-template <int E>
-__global__ __launch_bounds__(kTopkWaves * 64) void verify_topk_kernel(VerifyArgs a, int nc, double c, const uint32_t* cand) {
-    __shared__ uint32_t scratch[kTopkWaves][64 * E];
-    __shared__ double s_p[kMaxDraft + 1][64];
-    __shared__ int s_index[kMaxDraft + 1][64];
-    __shared__ int s_ok[kMaxDraft + 1];
-    __shared__ int s_token;
-    __shared__ int s_qi[64];
-    __shared__ float s_qp[64];
+// One workgroup per sequence, W waves per row.  cand null: rows are read as they
+// are.  A wave whose drafted token is refused draws the token that comes out if
+// all before it stand, so that nothing but tokens meets at the end.
+template <int E, int W>
+__global__ __launch_bounds__(kRowsAtOnce * W * 64) void verify_topk_kernel(VerifyArgs a, int nc, double c, const uint32_t* cand) {
+    __shared__ uint32_t scratch[kRowsAtOnce * W][64 * E];
+    __shared__ uint32_t s_list[W == 2 ? kRowsAtOnce * 64 : 1];
+    __shared__ int s_token[kMaxDraft + 1];              // drawn at row i, or kStands
+    constexpr int kStands = -2;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int b = blockIdx.x, n = drafted(a, b), k = a.top_k;
+    const int b = blockIdx.x, n = drafted(a, b), k = a.top_k, D = a.D;
+    const int slot = wave / W, part = wave % W;
 
-    for (int i = wave; i <= n; i += kTopkWaves) {
-        const size_t row = (size_t)b * (a.D + 1) + i;
+    for (int i0 = 0; i0 <= n; i0 += kRowsAtOnce) {
+        const int i = i0 + slot;
+        if (i > n) {
+            if constexpr (W == 2) {
+                __syncthreads();
+                __syncthreads();
+            }
+            break;
+        }
+        const size_t row = (size_t)b * (D + 1) + i;
         uint32_t v[E];
+        auto at = [&](int j) { return lane + 64 * (W * j + part); };
         if (cand) {
-            const uint32_t* cr = cand + row * nc;
+            const auto cr = make_rsrc(cand + row * nc, (uint32_t)nc * 4);
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = cr[lane + 64 * j < nc ? lane + 64 * j : 0];
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = lane + 64 * j < nc ? v[j] : 0u;
+            for (int j = 0; j < E; ++j) v[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(cr, 4 * at(j), 0, 0);      // (0 behind the end)
         } else {
-            const uint16_t* lg = a.logits + row * a.V;
+            const auto lg = make_rsrc(a.logits + row * a.V, (uint32_t)a.V * 2);
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = lg[lane + 64 * j < a.V ? lane + 64 * j : 0];
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = lane + 64 * j < a.V ? entry_of(v[j], lane + 64 * j) : 0u;
+            for (int j = 0; j < E; ++j) v[j] = buf_load2(lg, (uint32_t)(2 * at(j)), 0);
         }
-        const uint32_t e = wave_topk_sorted<E, true>(v, k, scratch[wave], lane);
-        const int index = (int)(0xFFFFu - (e & 0xFFFFu));
-        const double p = topk_prob64(e, k, c, lane);
-        s_p[i][lane] = p;
-        s_index[i][lane] = index;
-        if (i == n) continue;
-        const int d = a.draft[(size_t)b * a.D + i];
-        const double pd = wave_sum(index == d ? p : 0.0);
-        double qd = 1.0;
-        if (a.draft_index) {
-            const size_t at = ((size_t)b * a.D + i) * a.draft_k;
-            qd = wave_sum(lane < a.draft_k && a.draft_index[at + lane] == d ? (double)a.draft_prob[at + lane] : 0.0);
-        }
-        if (lane == 0) {
-            s_ok[i] = (double)a.u[(size_t)b * (a.D + 1) + i] * qd < pd;
-            if (a.accept_prob) a.accept_prob[(size_t)b * a.D + i] = accept_ratio(pd, qd);
-        }
-    }
-    if (a.accept_prob && tid >= n && tid < a.D) a.accept_prob[(size_t)b * a.D + tid] = 0.f;
-    __syncthreads();
-    int stand = 0;
-    while (stand < n && s_ok[stand]) ++stand;
-    if (wave == 0) {
-        const int index = s_index[stand][lane];
-        const double p = s_p[stand][lane];
-        double q = 0.0;
-        if (stand < n) {
-            if (a.draft_index) {
-                const size_t at = ((size_t)b * a.D + stand) * a.draft_k;
-                if (lane < a.draft_k) {
-                    s_qi[lane] = a.draft_index[at + lane];
-                    s_qp[lane] = a.draft_prob[at + lane];
-                }
-                __builtin_amdgcn_wave_barrier();
-                for (int i = 0; i < a.draft_k; ++i) q += s_qi[i] == index ? (double)s_qp[i] : 0.0;
-            } else {
-                q = index == a.draft[(size_t)b * a.D + stand] ? 1.0 : 0.0;
+        // the draft's side, asked for before the selection
+        int d = -1, qi = -1;
+        float qp = 0.f, ui = 0.f;
+        const float ud = a.u[(size_t)b * (D + 1) + D];
+        if (i < n) {
+            d = a.draft[(size_t)b * D + i];
+            ui = a.u[row];
+            if (a.draft_index && lane < a.draft_k) {
+                const size_t l = ((size_t)b * D + i) * a.draft_k + lane;
+                qi = a.draft_index[l];
+                qp = a.draft_prob[l];
             }
         }
-        double g = __builtin_fmax(p - q, 0.0);
-        if (!(wave_sum(g) > 0.0)) g = p;
-        const double run = wave_scan(g, lane), total = lane_value(run, 63);
-        const double x = (double)a.u[(size_t)b * (a.D + 1) + a.D] * total;
-        const unsigned long long over = __ballot(run > x && g > 0.0), any = __ballot(g > 0.0);
-        const int pick = over ? (int)__builtin_ctzll(over) : any ? 63 - (int)__builtin_clzll(any) : -1;
-        const int token = pick < 0 ? -1 : __shfl(index, pick);
-        if (lane == 0) s_token = token;
+        if (!cand) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = at(j) < a.V ? entry_of(v[j], at(j)) : 0u;
+        }
+        uint32_t e;
+        if constexpr (W == 1) {
+            e = wave_topk_sorted<E, true>(v, k, scratch[wave], lane);
+        } else {
+            __syncthreads();
+            if (part) s_list[64 * slot + lane] = wave_topk_sorted<E, false>(v, k, scratch[wave], lane);
+            else e = wave_topk_sorted<E, true>(v, k, scratch[wave], lane);
+            __syncthreads();
+            if (part) continue;
+            e = merge_top64<true>(e, s_list[64 * slot + lane], lane);
+        }
+        const int index = (int)(0xFFFFu - (e & 0xFFFFu));
+        double g = topk_prob64(e, k, c, lane);
+        bool stands = false;
+        if (i < n) {
+            const double pd = wave_sum(index == d ? g : 0.0), qd = a.draft_index ? wave_sum(qi == d ? (double)qp : 0.0) : 1.0;
+            stands = (double)ui * qd < pd;
+            if (a.accept_prob && lane == 0) a.accept_prob[(size_t)b * D + i] = accept_ratio(pd, qd);
+            if (!stands) {
+                double q = 0.0;
+                if (a.draft_index) {
+#pragma unroll 4
+                    for (int l = 0; l < a.draft_k; ++l) {
+                        const float ql = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, qp), l));
+                        q += __builtin_amdgcn_readlane(qi, l) == index ? (double)ql : 0.0;
+                    }
+                } else {
+                    q = index == d ? 1.0 : 0.0;
+                }
+                const double rest = __builtin_fmax(g - q, 0.0);
+                if (__any(rest > 0.0)) g = rest;
+            }
+        }
+        int token = kStands;
+        if (!stands) {
+            const double run = wave_scan(g), x = (double)ud * lane_value(run, 63);
+            const unsigned long long over = __ballot(run > x && g > 0.0), any = __ballot(g > 0.0);
+            const int pick = over ? (int)__builtin_ctzll(over) : any ? 63 - (int)__builtin_clzll(any) : 0;
+            token = any ? __builtin_amdgcn_readlane(index, pick) : -1;
+        }
+        if (lane == 0) s_token[i] = token;
     }
+    if (a.accept_prob && tid >= n && tid < D) a.accept_prob[(size_t)b * D + tid] = 0.f;
     __syncthreads();
-    write_tokens(a, b, stand, s_token, tid);
+    if (wave == 0) {
+        const int mine = s_token[lane <= n ? lane : n];
+        const int stand = (int)__builtin_ctzll(__ballot(mine != kStands));
+        if (lane <= D) a.token[(size_t)b * (D + 1) + lane] = lane < stand ? a.draft[(size_t)b * D + lane] : lane == stand ? mine : -1;
+        if (lane == 0) a.count[b] = stand;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -239,7 +284,6 @@ __global__ __launch_bounds__(kTopkWaves * 64) void verify_topk_kernel(VerifyArgs
 // of 8 logits that touch it; the first and the last, where the row ends inside
 // them, value by value.
 // ---------------------------------------------------------------------------
-constexpr int kDrawJ = 2;      // adjacent groups of 8 logits per thread of the second launch (1 where the workgroups are few)
 constexpr int kSequences = (int)(kWsCounterBytes / kCtrStride);      // sequences of one pair of launches
 
 struct Row {
@@ -411,9 +455,7 @@ __device__ __forceinline__ void mass_end(const VerifyArgs& a, const MassBlock& m
     __shared__ double s_sum[4];
     __shared__ unsigned s_prev;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float m = top;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
+    float m = wave_max(top);
     if (lane == 0) s_top[wave] = m;
     __syncthreads();
     m = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
@@ -565,45 +607,39 @@ struct Part {
     double rest, all;    // sums of max(p - q, 0) and of p over a chunk
 };
 
-// The stop row's values of a thread's 8 J adjacent logits.
-template <int J>
+// The stop row's values of group g.
 struct Values {
-    double rest[8 * J], all[8 * J];
+    double rest[8], all[8];
 };
-template <int J>
-__device__ __forceinline__ void stop_values(const VerifyArgs& a, const Row& tr, const Row& dr, const Stop& st, double c, int g0, Values<J>& o) {
-    u32x4 z[J], y[J];
-    int g[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) g[j] = g0 + j;
-    load_groups<J>(tr, a.V, g, z);
+__device__ __forceinline__ void stop_values(const VerifyArgs& a, const Row& tr, const Row& dr, const Stop& st, double c, int g, Values& o) {
+    u32x4 z[1], y[1];
+    const int at[1] = {g};
+    load_groups<1>(tr, a.V, at, z);
     if (st.has_q) {
         if (dr.off == tr.off) {
-            load_groups<J>(dr, a.V, g, y);
+            load_groups<1>(dr, a.V, at, y);
         } else {        // the draft's row starts at another place of its group
-            uint32_t h[8 * J];
+            uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8 * J; ++e) {
-                const int i = 8 * g0 - tr.off + e;
+            for (int e = 0; e < 8; ++e) {
+                const int i = 8 * g - tr.off + e;
                 h[e] = dr.p[i < 0 ? 0 : i < a.V ? i : a.V - 1];       // (outside the row p is 0, whatever q)
             }
 #pragma unroll
-            for (int e = 0; e < 4 * J; ++e) y[e >> 2][e & 3] = h[2 * e] | (h[2 * e + 1] << 16);
+            for (int e = 0; e < 4; ++e) y[0][e] = h[2 * e] | (h[2 * e + 1] << 16);
         }
     }
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double p = prob(half_of(z[j], e), st.p_top, st.p_inv, c);
-            o.all[8 * j + e] = p;
-            if (st.has_q) o.rest[8 * j + e] = __builtin_fmax(p - prob(half_of(y[j], e), st.q_top, st.q_inv, c), 0.0);
-            else o.rest[8 * j + e] = 8 * (g0 + j) - tr.off + e == st.qtoken ? 0.0 : p;
-        }
+    for (int e = 0; e < 8; ++e) {
+        const double p = prob(half_of(z[0], e), st.p_top, st.p_inv, c);
+        o.all[e] = p;
+        if (st.has_q) o.rest[e] = __builtin_fmax(p - prob(half_of(y[0], e), st.q_top, st.q_inv, c), 0.0);
+        else o.rest[e] = 8 * g - tr.off + e == st.qtoken ? 0.0 : p;
+    }
 }
 
-// Block (b, chunk).
-template <int J>
+// Block (b, chunk); a chunk is a group per thread (two and four were no faster
+// anywhere: 32 sequences with V = 131072 51 us, 53 and 54 with the first launch).
 __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int chunks, double c, const Stop* stop, unsigned* cnt, Part* parts) {
     __shared__ double s_wave[2][4];
     __shared__ unsigned s_prev;
@@ -617,11 +653,11 @@ __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int c
     const Row tr = row_of(a.logits + ((size_t)b * (D + 1) + st.stand) * V, V);
     const Row dr = st.has_q ? row_of(a.draft_logits + ((size_t)b * D + st.stand) * V, V) : tr;
 
-    Values<J> v;
-    stop_values<J>(a, tr, dr, st, c, (chunk * kThreads + tid) * J, v);
+    Values v;
+    stop_values(a, tr, dr, st, c, chunk * kThreads + tid, v);
     double rest = 0.0, all = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8 * J; ++e) {
+    for (int e = 0; e < 8; ++e) {
         rest += v.rest[e];
         all += v.all[e];
     }
@@ -646,7 +682,7 @@ __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int c
         }
         const bool use_rest = __ballot(rs > 0.0) != 0;
         const double own = use_rest ? rs : as;
-        const double run = wave_scan(own, lane), total = lane_value(run, 63);
+        const double run = wave_scan(own), total = lane_value(run, 63);
         const double x = ru * total;
         const unsigned long long over = __ballot(run > x), any = __ballot(own > 0.0);
         const int l = over ? (int)__builtin_ctzll(over) : any ? 63 - (int)__builtin_clzll(any) : -1;
@@ -677,15 +713,15 @@ __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int c
         if (tid == 0) *token = -1;
         return;
     }
-    if (hit != chunk) stop_values<J>(a, tr, dr, st, c, (hit * kThreads + tid) * J, v);
+    if (hit != chunk) stop_values(a, tr, dr, st, c, hit * kThreads + tid, v);
     double own = 0.0;
     const bool use_rest = s_rest != 0;
 #pragma unroll
-    for (int e = 0; e < 8 * J; ++e) {
+    for (int e = 0; e < 8; ++e) {
         if (!use_rest) v.rest[e] = v.all[e];
         own += v.rest[e];
     }
-    const double run = wave_scan(own, lane), x = s_x;
+    const double run = wave_scan(own), x = s_x;
     if (lane == 63) s_wave[0][wave] = run;
     __syncthreads();
     double before = s_before;
@@ -694,9 +730,9 @@ __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int c
     // the first value whose running sum exceeds x; where rounding leaves none,
     // the chunk's last value above zero
     int first = 0x7FFFFFFF, last = -1;
-    const int i0 = 8 * (hit * kThreads + tid) * J - tr.off;
+    const int i0 = 8 * (hit * kThreads + tid) - tr.off;
 #pragma unroll
-    for (int e = 0; e < 8 * J; ++e) {
+    for (int e = 0; e < 8; ++e) {
         before += v.rest[e];
         if (v.rest[e] > 0.0) {
             if (before > x && first == 0x7FFFFFFF) first = i0 + e;
@@ -722,34 +758,47 @@ constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
+namespace {
+int topk_blocks(int V, int e) { return (V + kThreads * e - 1) / (kThreads * e); }
+// Long blocks share the two sorts of a wave between more logits: 48 sequences
+// with 4 drafted tokens, V = 16385, k = 30: 16.8, 14.2 and 13.4 us (both
+// launches) at 4, 8 and 16 logits per thread.  Too few workgroups to fill the
+// card take short ones: one sequence 8.6, 9.0 and 10.0 us.
+int topk_block_e(int B, int D, int V) {
+    return (size_t)B * (D + 1) * topk_blocks(V, kLongBlockE) >= 512 ? kLongBlockE : kBlockE;
+}
+}  // namespace
+
 // The workspace's first kWsCounterBytes are arrival counters (zero before and
 // after every call), everything after them is scratch.
 size_t verify_topk_ws_bytes(int B, int D, int V, int top_k) {
     if (V <= kDirectVocab) return 0;
-    const size_t nb = (V + kSplitBlock - 1) / kSplitBlock;
+    const size_t nb = topk_blocks(V, topk_block_e(B, D, V));
     return kWsCounterBytes + (size_t)B * (D + 1) * nb * top_k * 4;
 }
 
 hipError_t launch_verify_topk(const VerifyArgs& a, void* ws, hipStream_t s) {
     const double c = log2e_over(a.temperature);
-    const dim3 grid(a.B), block(kTopkWaves * 64);
+    const dim3 grid(a.B), block(kRowsAtOnce * 64), pairs(kRowsAtOnce * 2 * 64);
     if (a.V <= kDirectVocab) {
         const uint32_t* none = nullptr;
-        if (a.V <= 512) return launch_kernel(verify_topk_kernel<8>, grid, block, 0, s, a, 0, c, none);
-        return launch_kernel(verify_topk_kernel<kDirectE>, grid, block, 0, s, a, 0, c, none);
+        if (a.V <= 512) return launch_kernel(verify_topk_kernel<8, 1>, grid, block, 0, s, a, 0, c, none);
+        return launch_kernel(verify_topk_kernel<kPairE, 2>, grid, pairs, 0, s, a, 0, c, none);
     }
-    const int nb = (a.V + kSplitBlock - 1) / kSplitBlock, nc = nb * a.top_k;
+    const int be = topk_block_e(a.B, a.D, a.V), nb = topk_blocks(a.V, be), nc = nb * a.top_k;
     uint32_t* cand = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
-    hipError_t e = launch_kernel(block_topk_kernel, dim3((unsigned)(a.B * (a.D + 1) * nb)), dim3(kThreads), 0, s, a, nb, cand);
+    const dim3 first((unsigned)(a.B * (a.D + 1) * nb)), threads(kThreads);
+    hipError_t e = be == kBlockE ? launch_kernel(block_topk_kernel<kBlockE>, first, threads, 0, s, a, nb, cand)
+                                 : launch_kernel(block_topk_kernel<kLongBlockE>, first, threads, 0, s, a, nb, cand);
     if (e != hipSuccess) return e;
     const uint32_t* in = cand;
-    if (nc <= 512) return launch_kernel(verify_topk_kernel<8>, grid, block, 0, s, a, nc, c, in);
-    return launch_kernel(verify_topk_kernel<32>, grid, block, 0, s, a, nc, c, in);     // nc <= 30 * 64
+    if (nc <= 512) return launch_kernel(verify_topk_kernel<8, 1>, grid, block, 0, s, a, nc, c, in);
+    return launch_kernel(verify_topk_kernel<kPairE, 2>, grid, pairs, 0, s, a, nc, c, in);     // nc <= 30 * 64
 }
 
 namespace {
 struct FullPlan {
-    int rows, mass_steps, mass_j, draw_j;     // steps of the counting kernel (0: the other, groups per thread)
+    int rows, mass_steps, mass_j;     // steps of the counting kernel (0: the other, groups per thread)
     size_t mass_chunks, draw_chunks, stop_bytes, mass_bytes;
 };
 // Chunks of 256 J groups: as many groups per thread as leave the launch two
@@ -765,14 +814,13 @@ FullPlan full_plan(int B, int D, int V, bool drafts, bool aligned) {
     const size_t wanted = 512 / (size_t)b / p.rows + 1;
     p.mass_steps = 0;
     p.mass_j = chunks(4) >= wanted ? 4 : 1;
-    p.draw_j = (size_t)b * chunks(kDrawJ) < 512 ? 1 : kDrawJ;
     p.mass_chunks = chunks(p.mass_j);
     if (chunks(kHistJ) >= wanted && g >= 16 * kThreads) {       // both sides measured at row_mass_hist_kernel
         p.mass_chunks = chunks(kHistJ);
         p.mass_steps = (int)((g + kThreads * kHistStep * p.mass_chunks - 1) / (kThreads * kHistStep * p.mass_chunks));
         p.mass_chunks = chunks(p.mass_steps * kHistStep);
     }
-    p.draw_chunks = chunks(p.draw_j);
+    p.draw_chunks = chunks(1);
     p.stop_bytes = up256((size_t)b * sizeof(Stop));
     p.mass_bytes = up256((size_t)b * p.rows * p.mass_chunks * sizeof(Mass));
     return p;
@@ -819,8 +867,7 @@ hipError_t launch_verify_full(const VerifyArgs& args, void* ws, hipStream_t s) {
                                        : launch_kernel(row_mass_kernel<1>, first, block, 0, s, a, p.rows, mc, c, mass, cnt, stop);
         if (e != hipSuccess) return e;
         const Stop* st = stop;
-        e = p.draw_j == 1 ? launch_kernel(stop_draw_kernel<1>, second, block, 0, s, a, dc, c, st, cnt, parts)
-                          : launch_kernel(stop_draw_kernel<kDrawJ>, second, block, 0, s, a, dc, c, st, cnt, parts);
+        e = launch_kernel(stop_draw_kernel, second, block, 0, s, a, dc, c, st, cnt, parts);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

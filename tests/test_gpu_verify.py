@@ -68,7 +68,8 @@ def want_topk(lg, d, u, qi, qp, n, T, k):
 
 
 TOPK = [(1, 1, 1, 1, 0.8), (1, 4, 2049, 30, 0.8), (3, 2, 64, 64, 1.3), (5, 7, 513, 17, 0.5), (2, 63, 600, 30, 0.8), (4, 3, 2560, 64, 1.0),
-        (4, 3, 2561, 64, 1.0), (7, 5, 4097, 1, 0.8), (6, 4, 16385, 30, 0.8), (2, 7, 30720, 64, 0.8), (40, 8, 1025, 5, 1.0)]
+        (4, 3, 2561, 64, 1.0), (7, 5, 4097, 1, 0.8), (6, 4, 16385, 30, 0.8), (2, 7, 30720, 64, 0.8), (40, 8, 1025, 5, 1.0), (60, 4, 4097, 64, 0.8),
+        (30, 3, 16385, 30, 0.8)]
 
 
 @pytest.mark.parametrize("ties", [False, True])
