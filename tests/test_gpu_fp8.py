@@ -337,6 +337,21 @@ def test_gemm_nan_stays_in_its_row_and_column(q4):
         assert torch.equal(y[~want], clean[~want])
 
 
+def test_gemm_past_one_grid(q4):
+    """More workgroups than one grid holds, outputs past 2^32 bytes and elements."""
+    M, N, K = 1 << 18, (1 << 16) + 1, 128
+    print(f"gemm M={M} N={N} K={K}", flush=True)
+    x, xs, w, ws = operands(4096, N, K, 60)
+    reps = M // 4096
+    scale = torch.arange(1, reps + 1).repeat_interleave(4096)[:, None] / 64      # rows differ between repetitions
+    xg, xsg = gpu(x).repeat(reps, 1), gpu(xs).repeat(reps, 1) * scale.to("cuda", torch.float32)
+    y = q4.fp8b128_gemm(xg, xsg, gpu(w), gpu(ws))
+    rows = torch.tensor([0, 1, 4095, 4096, M // 2 - 1, M // 2, M // 2 + 1, 3 * M // 4, M - 64, M - 1])
+    ops = (xg[rows].cpu(), xsg[rows].cpu(), w, ws)
+    check_gemm(y[rows], ops)
+    del y, xg, xsg
+
+
 @pytest.mark.parametrize("M", [1, 16, 48, 100])
 def test_group_equals_single_calls(q4, M):
     """Projections that read one input, and one of another K, in one call."""
