@@ -770,11 +770,12 @@ int topk_block_e(int B, int D, int V) {
 }  // namespace
 
 // The workspace's first kWsCounterBytes are arrival counters (zero before and
-// after every call), everything after them is scratch.
+// after every call), everything after them is scratch.  Sizes grow with every
+// argument (here: as if all blocks were short), so that one made for the largest
+// batch serves every smaller one.
 size_t verify_topk_ws_bytes(int B, int D, int V, int top_k) {
     if (V <= kDirectVocab) return 0;
-    const size_t nb = topk_blocks(V, topk_block_e(B, D, V));
-    return kWsCounterBytes + (size_t)B * (D + 1) * nb * top_k * 4;
+    return kWsCounterBytes + (size_t)B * (D + 1) * topk_blocks(V, kBlockE) * top_k * 4;
 }
 
 hipError_t launch_verify_topk(const VerifyArgs& a, void* ws, hipStream_t s) {
@@ -827,16 +828,17 @@ FullPlan full_plan(int B, int D, int V, bool drafts, bool aligned) {
 }
 }  // namespace
 
-// Stops, masses by chunk, partial sums by chunk.
+// Stops, masses by chunk, partial sums by chunk.  The masses are at most
+//   2048 with one group per thread (4 x 512, as the next size leaves fewer than
+//        512 workgroups),
+//   4096 or 4 per row with four (8 x 512, or a row of under 4096 groups),
+//   a chunk of kHistJ groups each with the counting kernel.
 size_t verify_full_ws_bytes(int B, int D, int V) {
-    const int b = B < kSequences ? B : kSequences;
-    size_t most = 0;
-    for (int k = 0; k < 4; ++k) {
-        const FullPlan x = full_plan(B, D, V, k & 1, k & 2);
-        const size_t n = x.stop_bytes + x.mass_bytes + (size_t)b * x.draw_chunks * sizeof(Part);
-        most = n > most ? n : most;
-    }
-    return kWsCounterBytes + most;
+    const size_t b = B < kSequences ? B : kSequences, rows = b * (2 * D + 1), g = row_groups(V, false);
+    auto chunks = [&](int j) { return (g + (size_t)kThreads * j - 1) / ((size_t)kThreads * j); };
+    const size_t few = chunks(4) < 4 ? chunks(4) : 4, each = few > chunks(kHistJ) ? few : chunks(kHistJ);
+    const size_t masses = rows * each > 4096 ? rows * each : 4096;
+    return kWsCounterBytes + up256(b * sizeof(Stop)) + up256(masses * sizeof(Mass)) + b * chunks(1) * sizeof(Part);
 }
 
 hipError_t launch_verify_full(const VerifyArgs& args, void* ws, hipStream_t s) {

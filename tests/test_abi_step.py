@@ -133,6 +133,16 @@ def test_verify_workspace_sizes():
     assert f(32, 7, 131072) > f(32, 7, 16385) > f(1, 7, 16385)
 
 
+def test_verify_workspace_of_the_largest_batch_serves_smaller_ones():
+    for V in (2561, 5000, 16385, 30720):
+        sizes = [q4.verify_topk_workspace_bytes(B, 4, V, 30) for B in range(1, 200)]
+        assert sizes == sorted(sizes)
+    for D in (1, 7):
+        for V in (1, 2049, 16384, 16385, 32768, 50001, 131072, 1 << 20):
+            sizes = [q4.verify_full_workspace_bytes(B, D, V) for B in range(1, 600)]
+            assert sizes == sorted(sizes)
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
     x = torch.zeros(2, 128, dtype=torch.bfloat16)
