@@ -414,7 +414,8 @@ int bf16_head_sample_ws(const uint16_t* x, int M, int K, const uint16_t* w, int 
 /*
  * e4m3 codes and block scales of activations: h = x (up NULL), or
  * h = silu(x) * up in fp32 (the gated MLP's activation; silu(g) = g / (1 + e^-g),
- * taken as 0 for g below -87.3), x and up bf16 [M, K].  With a the largest |h| of a block of 128 columns:
+ * taken as 0 for g below -87.3), x and up bf16 [M, K].  With a the largest |h|
+ * of a block of 128 columns:
  *     scale[m, g] = RN(a / 448),  codes[m, k] = RN_e4m3(h[m, k] * 448 / a),
  * the quotient rounded once (exactly so without up); nothing saturates.  A
  * block of zeros has scale 0 and codes 0.  A value that is not finite (x, or
@@ -487,9 +488,9 @@ int fp8b128_workspace_bytes(const fp8b128_task* tasks, int count, int M, size_t*
  * q4_verify_*_workspace_bytes (where that is not 0), 256-byte aligned,
  * zero-filled before its first use; its first 64 KiB are arrival counters that
  * every call leaves at zero, the rest is scratch, so it can be shared with the
- * library's other calls that take a workspace of this kind.
- * Calls that use one workspace must not overlap in time.  Returns
- * Q4_EINVAL_PTR (no workspace where one is needed too), Q4_EINVAL_SHAPE,
+ * library's other calls that take a workspace of this kind.  Sizes grow with
+ * every argument: the largest batch's workspace serves smaller ones.  Calls
+ * that use one workspace must not overlap in time.  Returns Q4_EINVAL_PTR (no workspace where one is needed too), Q4_EINVAL_SHAPE,
  * Q4_EALIGN, Q4_ESCRATCH (workspace too small) or Q4_EALIAS before anything is
  * enqueued.
  */
