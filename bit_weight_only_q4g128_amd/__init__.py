@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -126,7 +127,7 @@ lib.bf16_head_sample_workspace_bytes.restype = ctypes.c_size_t
 
 
 class Fp8Task(ctypes.Structure):
-    """Mirror of the C struct fp8b128_task."""
+    """Mirror of the C struct fp8b128_task (an array of them, or its bytes)."""
     _fields_ = [("x", _p), ("xscale", _p), ("w", _p), ("wscale", _p), ("residual", _p), ("y", _p), ("N", _i), ("K", _i)]
 
 
@@ -134,9 +135,9 @@ lib.fp8b128_quantize.argtypes = [_p, _p, _i, _i, _p, _p, _p]
 lib.fp8b128_quantize.restype = ctypes.c_int
 lib.fp8b128_gemm.argtypes = [_p, _p, _i, _i, _p, _p, _i, _p, _p, _p]
 lib.fp8b128_gemm.restype = ctypes.c_int
-lib.fp8b128_gemm_grouped_ws.argtypes = [ctypes.POINTER(Fp8Task), _i, _i, _p, ctypes.c_size_t, _p]
+lib.fp8b128_gemm_grouped_ws.argtypes = [_p, _i, _i, _p, ctypes.c_size_t, _p]
 lib.fp8b128_gemm_grouped_ws.restype = ctypes.c_int
-lib.fp8b128_workspace_bytes.argtypes = [ctypes.POINTER(Fp8Task), _i, _i, ctypes.POINTER(ctypes.c_size_t)]
+lib.fp8b128_workspace_bytes.argtypes = [_p, _i, _i, ctypes.POINTER(ctypes.c_size_t)]
 lib.fp8b128_workspace_bytes.restype = ctypes.c_int
 lib.q4_verify_topk.argtypes = [_p, _i, _i, _i, _p, _p, _p, _i, _p, _p, _f, _i, _p, _p, _p, _p, ctypes.c_size_t, _p]
 lib.q4_verify_topk.restype = ctypes.c_int
@@ -633,6 +634,8 @@ def mixed_workspace_bytes(items) -> int:
 # ---------------------------------------------------------------------------
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _BLOCK = 128
+_FP8_TASK = struct.Struct("6Q2i").pack      # an Fp8Task's bytes (a tenth of the structure's own construction)
+assert ctypes.sizeof(Fp8Task) == 56
 # the raw handle of the current stream; building a Stream object costs as much
 # as a launch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -692,12 +695,18 @@ def fp8b128_quantize(x, up=None, codes=None, scale=None):
     shape, index = x.shape, x.get_device()
     M, K = shape
     G = (K + _BLOCK - 1) // _BLOCK
+    up_p = None if up is None else _tensor(up, "up", _U16, shape, index)
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        codes_p = codes.data_ptr()
+    else:
+        codes_p = _tensor(codes, "codes", _E4M3, shape, index)
     if scale is None:
         scale = x.new_empty((M, G), dtype=torch.float32)
-    _enqueue(index, lib.fp8b128_quantize, x.data_ptr(), _optional(up, "up", _U16, shape, index), M, K,
-             _tensor(codes, "codes", _E4M3, shape, index), _tensor(scale, "scale", _F32, (M, G), index))
+        scale_p = scale.data_ptr()
+    else:
+        scale_p = _tensor(scale, "scale", _F32, (M, G), index)
+    _enqueue(index, lib.fp8b128_quantize, x.data_ptr(), up_p, M, K, codes_p, scale_p)
     return codes, scale
 
 
@@ -706,10 +715,9 @@ def _fp8_task_array(items):
     count = len(items)
     if not 1 <= count <= 8:
         raise ValueError("1..8 tasks per call")
-    arr = (Fp8Task * count)()
-    outs, M, index = [], None, None
+    arr, outs, M, index = [], [], None, None
     last, last_scale = None, None
-    for i, (x, x_scale, w, w_scale, residual, out) in enumerate(items):
+    for x, x_scale, w, w_scale, residual, out in items:
         if x is not last or x_scale is not last_scale:
             _check(x, "x", _E4M3, 2)
             m, K = x.shape
@@ -725,11 +733,11 @@ def _fp8_task_array(items):
         N = w.shape[0]
         y = x_scale.new_empty((M, N), dtype=torch.bfloat16) if out is None else out
         outs.append(y)
-        arr[i] = Fp8Task(xp, sp, _tensor(w, "w", _E4M3, (N, K), index),
-                         _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), index),
-                         _optional(residual, "residual", _U16, (M, N), index),
-                         y.data_ptr() if out is None else _tensor(y, "out", _BF16, (M, N), index), N, K)
-    return arr, count, outs, M, index
+        arr.append(_FP8_TASK(xp, sp, _tensor(w, "w", _E4M3, (N, K), index),
+                             _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), index),
+                             0 if residual is None else _tensor(residual, "residual", _U16, (M, N), index),
+                             y.data_ptr() if out is None else _tensor(y, "out", _BF16, (M, N), index), N, K))
+    return b"".join(arr), count, outs, M, index
 
 
 def fp8b128_gemm_grouped(items, workspace=None):
@@ -793,11 +801,11 @@ def verify_topk(logits, draft, u, draft_index=None, draft_prob=None, n_draft=Non
         if not isinstance(draft_index, torch.Tensor) or draft_index.dim() != 3:
             raise ValueError("draft_index must be a tensor of 3 dims")
         kd = draft_index.shape[2]
-    up = _tensor(u, "u", _F32, (B, D1), index)
-    token = u.new_empty((B, D1), dtype=torch.int32)
+    up, dp = _tensor(u, "u", _F32, (B, D1), index), _tensor(draft, "draft", _I32, (B, D), index)
+    token = torch.empty_like(u, dtype=torch.int32)
     count = u.new_empty(B, dtype=torch.int32)
-    prob = u.new_empty((B, D))
-    _enqueue(index, lib.q4_verify_topk, logits.data_ptr(), B, D, V, _tensor(draft, "draft", _I32, (B, D), index),
+    prob = torch.empty_like(draft, dtype=torch.float32)
+    _enqueue(index, lib.q4_verify_topk, logits.data_ptr(), B, D, V, dp,
              _optional(draft_index, "draft_index", _I32, (B, D, kd), index),
              _optional(draft_prob, "draft_prob", _F32, (B, D, kd), index), kd, _optional(n_draft, "n_draft", _I32, (B,), index),
              up, temperature, top_k, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
@@ -814,11 +822,11 @@ def verify_full(logits, draft, u, draft_logits=None, n_draft=None, temperature: 
     D, index = D1 - 1, logits.get_device()
     if workspace is None:
         workspace = logits.new_zeros(verify_full_workspace_bytes(B, D, V), dtype=torch.uint8)
-    up = _tensor(u, "u", _F32, (B, D1), index)
-    token = u.new_empty((B, D1), dtype=torch.int32)
+    up, dp = _tensor(u, "u", _F32, (B, D1), index), _tensor(draft, "draft", _I32, (B, D), index)
+    token = torch.empty_like(u, dtype=torch.int32)
     count = u.new_empty(B, dtype=torch.int32)
-    prob = u.new_empty((B, D))
-    _enqueue(index, lib.q4_verify_full, logits.data_ptr(), B, D, V, _tensor(draft, "draft", _I32, (B, D), index),
+    prob = torch.empty_like(draft, dtype=torch.float32)
+    _enqueue(index, lib.q4_verify_full, logits.data_ptr(), B, D, V, dp,
              _optional(draft_logits, "draft_logits", _U16, (B, D, V), index), _optional(n_draft, "n_draft", _I32, (B,), index),
              up, temperature, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
              *_scratch(workspace, index))

@@ -645,6 +645,7 @@ const Kind kTiles[] = {
     {256, 256, 8, 0, 1, 14.0f, {1.604f}, 4, go_tile<256, 256, 4, 2>},
 };
 constexpr int kCUs = 256;
+constexpr int kMostSlices = 16;
 
 struct Plan {
     const Kind* kind;
@@ -657,65 +658,65 @@ long tiles_of(const Kind& k, int N, int M) { return (long)((N + k.bn - 1) / k.bn
 
 // Workspace bytes of a plan's splits (0: none), or SIZE_MAX where its tiles
 // have too few counters.
-size_t plan_ws(const Kind& k, const Fp8Args* t, int count, int M, const int* ks) {
-    size_t part = 0, tiles = 0;
+size_t plan_ws(const Kind& k, const long* tiles, int count, const int* ks) {
+    size_t part = 0, split = 0;
     for (int i = 0; i < count; ++i)
         if (ks[i] > 1) {
-            part += (size_t)tiles_of(k, t[i].N, M) * ks[i] * k.waves * k.frags * 1024;
-            tiles += tiles_of(k, t[i].N, M);
+            part += (size_t)tiles[i] * ks[i] * k.waves * k.frags * 1024;
+            split += tiles[i];
         }
     if (!part) return 0;
-    return tiles * kCtrStride > kWsCounterBytes ? SIZE_MAX : kWsCounterBytes + part;
+    return split * kCtrStride > kWsCounterBytes ? SIZE_MAX : kWsCounterBytes + part;
 }
 
-// Modelled time (us) of kind k with up to `split` slices of K per task.
-double plan_time(const Kind& k, const Fp8Args* t, int count, int M, int split, int* ks) {
-    long groups = 0;
-    double steps = 0, work = 0, bytes = 0;
+// Modelled time (us) of kind k with ks slices of K per task (G blocks each) and
+// ws bytes of workspace; bytes: of all operands and outputs.
+double plan_time(const Kind& k, const long* tiles, const int* G, int count, const int* ks, size_t ws, double bytes) {
+    long groups = 0, steps = 0, work = 0;
     for (int i = 0; i < count; ++i) {
-        const int G = blocks_of(t[i].K);
-        const long tiles = tiles_of(k, t[i].N, M);
-        ks[i] = 1;
-        while (2 * ks[i] <= split && G / (2 * ks[i]) >= k.min_blocks) ks[i] *= 2;
-        const double s = (double)((G + ks[i] - 1) / ks[i]);
-        groups += tiles * ks[i];
-        work += tiles * ks[i] * s;
+        const long s = (G[i] + ks[i] - 1) / ks[i], n = tiles[i] * ks[i];
+        groups += n;
+        work += n * s;
         steps = s > steps ? s : steps;
-        bytes += (double)t[i].N * t[i].K + (double)M * t[i].K + 2.0 * M * t[i].N;
     }
     // whole rounds of resident workgroups, then the rest; workgroups of
     // unequal length even out
     const int r = k.resident;
-    const double mean = work / groups;
+    const double mean = (double)work / groups;
     const long full = groups / (kCUs * r), rest = groups - full * kCUs * r;
     double run = full * mean * k.block[r - 1];
     if (rest) run += (full ? mean : steps) * k.block[(rest + kCUs - 1) / kCUs - 1];
     // a further round fills its stages and stores its tiles anew
     run += (full + (rest > 0) - 1) * (r == 1 ? k.fixed - 3.5 : 2.0);
     const double memory = bytes / 4.6e6;
-    const size_t part = plan_ws(k, t, count, M, ks);
-    const double join = part ? 1.8 + 2.0 * (double)part / 8e6 : 0.0;
+    const double join = ws ? 1.8 + 2.0 * (double)(ws - kWsCounterBytes) / 8e6 : 0.0;
     return k.fixed + (run > memory ? run : memory) + join;
 }
 
 Plan plan_of(const Fp8Args* t, int count, int M, size_t ws_bytes) {
     Plan p{};
-    int G = blocks_of(t[0].K);
-    long n = 0;
+    int G[kFp8MaxTasks], least = 1 << 30;
+    long tiles[kFp8MaxTasks], n = 0;
+    double bytes = 0;
     for (int i = 0; i < count; ++i) {
         p.ks[i] = 1;
         n += t[i].N;
-        G = blocks_of(t[i].K) < G ? blocks_of(t[i].K) : G;
+        G[i] = blocks_of(t[i].K);
+        least = G[i] < least ? G[i] : least;
+        bytes += (double)t[i].N * t[i].K + (double)M * t[i].K + 2.0 * M * t[i].N;
     }
     // Up to one batch tile, and weights that give each CU no more than one such
     // workgroup (or long rows): the waves load for themselves, with no stages
     // to fill first (M = 1: N = K = 2048 4.5 us, in tiles 6.2; 8 x 8192 x 8192
     // 15.9 and 19.0; but N = 16385, K = 2048 11.0 and 9.0).
-    if (M <= 16 && (n <= 32 * kCUs || G >= 32)) {
+    if (M <= 16 && (n <= 32 * kCUs || least >= 32)) {
         p.kind = n <= 16 * kCUs || n > 32 * kCUs ? &kRows16 : &kRows32;
-        if (n <= 8 * kCUs && G >= 32) {      // half the CUs: two slices (2048 x 8192: 7.2 us, unsplit 7.8)
-            for (int i = 0; i < count; ++i) p.ks[i] = 2;
-            p.ws = plan_ws(*p.kind, t, count, M, p.ks);
+        if (n <= 8 * kCUs && least >= 32) {      // half the CUs: two slices (2048 x 8192: 7.2 us, unsplit 7.8)
+            for (int i = 0; i < count; ++i) {
+                p.ks[i] = 2;
+                tiles[i] = tiles_of(*p.kind, t[i].N, M);
+            }
+            p.ws = plan_ws(*p.kind, tiles, count, p.ks);
             if (p.ws > ws_bytes) {
                 for (int i = 0; i < count; ++i) p.ks[i] = 1;
                 p.ws = 0;
@@ -723,23 +724,38 @@ Plan plan_of(const Fp8Args* t, int count, int M, size_t ws_bytes) {
         }
         return p;
     }
-    if (G < 4) {
+    if (least < 4) {
         p.kind = M <= 16 ? &kRows16 : &kRows64;
         return p;
     }
     double best = 0;
-    for (const Kind& k : kTiles)
-        for (int split = 1; split <= 16; split *= 2) {
-            if (split > 1 && !k.frags) break;
-            int ks[kFp8MaxTasks] = {};
-            const double time = plan_time(k, t, count, M, split, ks);
-            const size_t ws = plan_ws(k, t, count, M, ks);
-            if (ws > ws_bytes || (p.kind && time >= best)) continue;
-            best = time;
-            p.kind = &k;
-            p.ws = ws;
-            for (int i = 0; i < count; ++i) p.ks[i] = ks[i];
+    for (const Kind& k : kTiles) {
+        int ks[kFp8MaxTasks];
+        for (int i = 0; i < count; ++i) {
+            ks[i] = 1;
+            tiles[i] = tiles_of(k, t[i].N, M);
         }
+        for (bool more = true; more;) {
+            const size_t ws = plan_ws(k, tiles, count, ks);
+            if (ws == SIZE_MAX) break;
+            if (ws <= ws_bytes) {
+                const double time = plan_time(k, tiles, G, count, ks, ws, bytes);
+                if (!p.kind || time < best) {
+                    best = time;
+                    p.kind = &k;
+                    p.ws = ws;
+                    for (int i = 0; i < count; ++i) p.ks[i] = ks[i];
+                }
+            }
+            // twice the slices, where a task's stay long enough
+            more = false;
+            for (int i = 0; k.frags && i < count; ++i)
+                if (ks[i] <= kMostSlices / 2 && G[i] / (2 * ks[i]) >= k.min_blocks) {
+                    ks[i] *= 2;
+                    more = true;
+                }
+        }
+    }
     return p;
 }
 
