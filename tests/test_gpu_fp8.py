@@ -148,6 +148,21 @@ def test_quantize_gated_extremes(q4):
     assert sc[1, 0] < 1e-30 and sc[4, 0] == 0
 
 
+def test_quantize_past_32_bit_offsets(q4):
+    """More than 2^32 values: rows at both ends and around 2^31 and 2^32."""
+    M, K = 1 << 19, 8208
+    print(f"quantize M={M} K={K}", flush=True)
+    rows = [0, 1, (1 << 31) // K, (1 << 31) // K + 1, (1 << 32) // K - 1, (1 << 32) // K, (1 << 32) // K + 1, M - 2, M - 1]
+    some = activations(len(rows), K, 8)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[rows] = gpu(some)
+    codes, scale = q4.fp8b128_quantize(x)
+    check_plain(codes[rows], scale[rows], synth.bits16(some))
+    others = [2, (1 << 32) // K + 2, M - 3]
+    assert int(codes.view(torch.uint8)[others].count_nonzero()) == 0 and int(scale[others].count_nonzero()) == 0
+    del x, codes, scale
+
+
 def test_quantize_into_outputs(q4):
     """Given outputs are written whole and nothing beside them."""
     M, K = 5, 400

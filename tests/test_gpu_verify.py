@@ -277,6 +277,35 @@ def test_stream_and_graph(q4, form):
     del graph
 
 
+def test_calls_at_once_on_their_own_workspaces(q4):
+    """Both forms and a second batch of one of them on three streams at a time."""
+    T, k = 0.8, 30
+    cases = []
+    for seed, (B, D, V) in enumerate(((6, 4, 16385), (90, 3, 33001), (20, 4, 16385))):
+        lg, dl, u, n, g = inputs(B, D, V, 40 + seed)
+        full = seed < 2
+        qi, qp, d = (None, None, drawn_of(dl, T, g)) if full else lists_of(dl, T, k, g)
+        ws = torch.zeros(q4.verify_full_workspace_bytes(B, D, V) if full else q4.verify_topk_workspace_bytes(B, D, V, k),
+                         dtype=torch.uint8, device="cuda")
+        a = [None if t is None else gpu(t) for t in (lg, d, u, qi, qp, dl, n)]
+
+        def call(a=a, ws=ws, full=full):
+            if full:
+                return q4.verify_full(a[0], a[1], a[2], draft_logits=a[5], n_draft=a[6], temperature=T, workspace=ws)
+            return q4.verify_topk(a[0], a[1], a[2], draft_index=a[3], draft_prob=a[4], n_draft=a[6], temperature=T, top_k=k, workspace=ws)
+
+        cases.append((call, [t.clone() for t in call()], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for rep in range(8):
+        outs = []
+        for call, _, stream in cases:
+            with torch.cuda.stream(stream):
+                outs.append(call())
+        torch.cuda.synchronize()
+        for got, (_, want, _) in zip(outs, cases):
+            assert all(torch.equal(x, y) for x, y in zip(got, want)), f"repetition {rep}"
+
+
 def test_draft_and_verify_step(q4):
     """The operators as a step uses them: hidden states of every drafted
     position quantised, the head's 8-bit product, the draft's tokens from the
