@@ -120,9 +120,16 @@ __device__ __forceinline__ float accept_ratio(double p, double q) {
 
 // ---------------------------------------------------------------------------
 // top-k form.  Rows of at most kDirectVocab logits: one launch, a workgroup
-// per sequence, a wave per row.  Longer rows: a first launch takes the top k
-// of every block of 1024 or 4096, and the waves of the second merge a row's
+// per sequence, one or two waves per row.  Longer rows: a first launch takes the
+// top k of every block of 1024 or 4096, and the second merges a row's
 // candidates.  Nothing is handed over inside a launch.
+//
+// Bound by latency and, for many rows, by the selection's instructions (about
+// 550 per wave and block, half of them two sorts of 64), not by the 2 bytes per
+// logit: one sequence with 4 drafted tokens, V = 2049, k = 30: 7.6 us, of which a
+// launch is 1.5 and the logits' round trip about 2; 48 sequences, V = 16385: 8.6
+// and 5.1 us.  Two waves share a row above 512 logits or candidates: V = 2049 in
+// a graph 9.3 us, one wave with 40 logits per lane 12.5; V = 300 5.2 us in one.
 // ---------------------------------------------------------------------------
 constexpr int kRowsAtOnce = 8;                      // of a workgroup of the last launch
 constexpr int kPairE = 20;                          // entries per lane of two waves that share a row
@@ -279,6 +286,12 @@ __global__ __launch_bounds__(kRowsAtOnce * W * 64) void verify_topk_kernel(Verif
 // that ends a sequence's last chunk verifies its drafted tokens.  Second
 // launch: the sums of max(p - q, 0) and of p over the chunks of each sequence's
 // stop row; the last one finds the chunk, then the entry, that the draw hits.
+//
+// Few sequences are bound by latency: one with 4 drafted tokens, V = 16385: 5.9
+// and 6.0 us, each a launch, one round of loads, the arrival (about 2 us) and
+// what the last workgroup does alone.  Many are bound by memory, and that at the
+// ends: 32 with 7, V = 131072: 33 us for 101 to 126 MB, then 16 us, of which the
+// stop rows' 15 MB are about 5.
 //
 // A row starts at any even address.  It is read as the 16-byte aligned groups
 // of 8 logits that touch it; the first and the last, where the row ends inside
