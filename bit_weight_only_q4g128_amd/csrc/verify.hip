@@ -485,7 +485,9 @@ __device__ __forceinline__ void mass_end(const VerifyArgs& a, const MassBlock& m
     accept(a, mb.b, mb.n, chunks, c, mine, stop + mb.b, tid);
 }
 
-// Short rows: J groups per thread, one exponential per logit.
+// Short rows: J groups per thread, one exponential per logit.  (z - top first:
+// with z c and top c apart, rows that hold a mask's far value alone would keep
+// the products' rounding, up to 2^75.)
 template <int J>
 __global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int rows, int chunks, double c, Mass* mass, unsigned* cnt,
                                                             Stop* stop) {
@@ -502,11 +504,10 @@ __global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int ro
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, half_of(v[j], e));
     double sum = 0.0;
-    const double base = -(double)top * c;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += exp2_raw(__builtin_fma((double)half_of(v[j], e), c, base));
+        for (int e = 0; e < 8; ++e) sum += exp2_raw(((double)half_of(v[j], e) - (double)top) * c);
     mass_end(a, mb, top, sum, rows, chunks, c, mass, cnt, stop);
 }
 

@@ -222,6 +222,34 @@ def test_full_long_rows_of_many_sequences(q4, V):
     check(run_full(q4, lg, d, u, dl, n, T), want_full(lg, d, u, dl, n, T))
 
 
+@pytest.mark.parametrize("form,B,V", [("full", 8, 301), ("full", 8, 5001), ("full", 24, 16384), ("full", 80, 33001), ("topk", 8, 301),
+                                      ("topk", 8, 2049), ("topk", 8, 16385), ("topk", 300, 5001)])
+@pytest.mark.parametrize("T", [0.7, 1.3])
+def test_masked_rows(q4, form, B, V, T):
+    """Rows whose logits are all, or all but a few, a mask's value: the type's
+    lowest, the largest and other far values."""
+    D, k = 3, 30
+    print(f"{form} B={B} V={V} T={T}", flush=True)
+    lg, dl, u, n, g = inputs(B, D, V, 12)
+    n[:8] = D
+    for b, value in enumerate((torch.finfo(torch.bfloat16).min, -1e30, -65504.0, torch.finfo(torch.bfloat16).max)):
+        lg[b], dl[b] = value, value
+        keep = torch.rand(V, generator=g) < 0.02
+        lg[4 + b, :, ~keep], dl[4 + b, :, ~keep] = value, value
+    p, i = torch.softmax(dl.double() / T, -1), None
+    if form == "topk":
+        p, i = torch.sort(p, dim=-1, descending=True, stable=True)
+        p, i = (p[..., :k] / p[..., :k].sum(-1, keepdim=True)).float(), i[..., :k].to(torch.int32).contiguous()
+    d = torch.multinomial(p.view(B * D, -1), 1, generator=g).view(B, D, 1)
+    if form == "full":
+        d = d[..., 0].to(torch.int32).contiguous()
+        check(run_full(q4, lg, d, u, dl, n, T), want_full(lg, d, u, dl, n, T))
+        check(run_full(q4, lg, d, u, None, n, T), want_full(lg, d, u, None, n, T))
+    else:
+        d = i.gather(2, d)[..., 0].contiguous()
+        check(run_topk(q4, lg, d, u, i, p, n, T, k), want_topk(lg, d, u, i, p, n, T, k))
+
+
 def test_dirty_shared_workspace(q4):
     """One workspace for both forms and for products, its scratch full of
     rubbish, its first 64 KiB left as they are."""
