@@ -403,7 +403,9 @@ int bf16_head_sample_ws(const uint16_t* x, int M, int K, const uint16_t* w, int 
  * consecutive columns' products aligned to the largest of them (what lies below
  * 2^-13 of it is dropped) and those sums in fp32; blocks are added in fp32, in
  * a fixed order, so results do not change from call to call, and rounded to
- * bf16 once.  NaN codes and scales make the outputs they reach NaN.
+ * bf16 once.  xscale wscale is an fp32 product: scales so far from 1 that
+ * it leaves the normal range lose accuracy or give 0 or infinity.  NaN codes and
+ * scales make the outputs they reach NaN.
  *
  * Limits: 1 <= M <= 524288, 1 <= N <= 2^24, 16 <= K <= 32768, K % 16 == 0;
  * x, w and codes 16-byte aligned, scales 4, y and residual 2.  residual may be
