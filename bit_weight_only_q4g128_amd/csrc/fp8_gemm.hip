@@ -16,6 +16,8 @@
 // column l % 16 (a batch row), 32 of the block's columns each; the order of
 // the columns within a block is free as long as both operands share it.  D:
 // lane l holds weight rows 4 (l / 16) + v, v = 0..3, of batch row l % 16.
+#include <iterator>
+
 #include "fp8.h"
 #include "internal.h"
 #include "topk.h"
@@ -185,46 +187,43 @@ __device__ __forceinline__ bool join(f32x4 (&v)[NF], const Fp8Group& p, const Wh
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a workgroup of eight waves owns 16 R weight rows and 16 MT batch
-// rows over a slice of K; the waves share the slice's blocks, each loading its
+// Few rows: a workgroup of eight waves owns 16 R weight rows and 16 batch rows
+// over a slice of K; the waves share the slice's blocks, each loading its
 // own fragments straight into registers, and meet in LDS.  Bound by the latency
 // of a launch and of one round of loads: 1 x 2048 x 8192 (M x N x K) 7.4 us for
 // 16.8 MB, 1 x 2048 x 2048 4.5 us; at 8 x 8192 x 8192 17 us, 3.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 
-template <int MT, int R>
+template <int R>
 __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
-    constexpr int kTiles = R * MT, kMine = (kTiles + kWaves - 1) / kWaves;
-    constexpr int U = R * MT <= 4 ? 4 : 2;     // blocks whose loads are in flight together
-    __shared__ __attribute__((aligned(16))) f32x4 part[kWaves][kTiles][64];
+    constexpr int U = 4;     // blocks whose loads are in flight together
+    __shared__ __attribute__((aligned(16))) f32x4 part[kWaves][R][64];
     __shared__ __attribute__((aligned(16))) float turn[kWaves][16 * 20];
     __shared__ unsigned s_prev;
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Where at = where(p, blockIdx.x);
     const Fp8Args a = p.t[at.task];
-    const Block blk = block_of(at.tile, (p.M + 16 * MT - 1) / (16 * MT), (a.N + 16 * R - 1) / (16 * R));
-    const int n0 = blk.n * 16 * R, m0 = blk.m * 16 * MT;
+    const Block blk = block_of(at.tile, (p.M + 15) / 16, (a.N + 16 * R - 1) / (16 * R));
+    const int n0 = blk.n * 16 * R, m0 = blk.m * 16;
     const int K = a.K, G = (K + 127) >> 7;
-    const int rows_n = a.N - n0 < 16 * R ? a.N - n0 : 16 * R, rows_m = p.M - m0 < 16 * MT ? p.M - m0 : 16 * MT;
+    const int rows_n = a.N - n0 < 16 * R ? a.N - n0 : 16 * R, rows_m = p.M - m0 < 16 ? p.M - m0 : 16;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (uint32_t)rows_n * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (uint32_t)rows_m * (uint32_t)K);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
     const const_float* wsrow = (const const_float*)(uintptr_t)(a.ws + (size_t)(n0 >> 7) * G);      // (16 R divides 128: one row)
 
-    f32x4 acc[R][MT];
+    f32x4 acc[R];
 #pragma unroll
-    for (int t = 0; t < R; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < R; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int ks = p.ks[at.task];
     const int b0 = G * at.slice / ks, b1 = G * (at.slice + 1) / ks;
     const int g0 = b0 + (b1 - b0) * wave / kWaves, g1 = b0 + (b1 - b0) * (wave + 1) / kWaves;
     for (int gu = g0; gu < g1; gu += U) {
-        u32x4 wf[U][R][2], xf[U][MT][2];
-        float f[U][MT];
+        u32x4 wf[U][R][2], xf[U][2];
+        float f[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             // a row past the matrix, a column past K and a block past the
@@ -238,51 +237,30 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
                 for (int c = 0; c < 2; ++c)
                     wf[j][t][c] = ld16(rw, in && k + 64 * c < (uint32_t)K ? (uint32_t)(16 * t + lr) * K + k + 64 * c : 0xFFFFFFF0u);
 #pragma unroll
-            for (int u = 0; u < MT; ++u) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    xf[j][u][c] = ld16(rx, in && k + 64 * c < (uint32_t)K ? (uint32_t)(16 * u + lr) * K + k + 64 * c : 0xFFFFFFF0u);
-                f[j][u] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                        rs, in ? (int)(((16 * u + lr) * G + g) * 4) : (int)0xFFFFFFF0u, 0, 0));
-            }
+            for (int c = 0; c < 2; ++c)
+                xf[j][c] = ld16(rx, in && k + 64 * c < (uint32_t)K ? (uint32_t)lr * K + k + 64 * c : 0xFFFFFFF0u);
+            f[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, in ? (lr * G + g) * 4 : (int)0xFFFFFFF0u, 0, 0));
         }
         __builtin_amdgcn_sched_barrier(0);      // every load is on its way before the first wait
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const float s = wsrow[gu + j < g1 ? gu + j : g1 - 1];
+            const float sw = wsrow[gu + j < g1 ? gu + j : g1 - 1], fs = f[j] * (gu + j < g1 ? sw : 0.0f);      // (sw may be infinite)
 #pragma unroll
-            for (int u = 0; u < MT; ++u) {
-                const float fs = f[j][u] * s;
+            for (int t = 0; t < R; ++t) {
+                const f32x4 d = mfma(wf[j][t], xf[j]);
 #pragma unroll
-                for (int t = 0; t < R; ++t) {
-                    const f32x4 d = mfma(wf[j][t], xf[j][u]);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[t][u][v] = __builtin_fmaf(fs, d[v], acc[t][u][v]);
-                }
+                for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(fs, d[v], acc[t][v]);
             }
         }
     }
 #pragma unroll
-    for (int t = 0; t < R; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) part[wave][t * MT + u][lane] = acc[t][u];
+    for (int t = 0; t < R; ++t) part[wave][t][lane] = acc[t];
     __syncthreads();
-    f32x4 v[kMine];
+    f32x4 v[1] = {part[0][wave < R ? wave : 0][lane]};
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int q = wave + kWaves * j < kTiles ? wave + kWaves * j : 0;
-        v[j] = part[0][q][lane];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) v[j] += part[w][q][lane];
-    }
-    if (ks > 1 && !join(v, p, at, kTiles < kWaves ? kTiles : kWaves, wave, lane, &s_prev)) return;
-    if (wave >= kTiles) return;
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int q = wave + kWaves * j;
-        if (q < kTiles)
-            store_tile<1, 1>(&v[j], reinterpret_cast<uint8_t*>(turn), a.resid, a.y, p.M, a.N, m0 + 16 * (q % MT), n0 + 16 * (q / MT), wave, lane);
-    }
+    for (int w = 1; w < kWaves; ++w) v[0] += part[w][wave < R ? wave : 0][lane];
+    if (ks > 1 && !join(v, p, at, R, wave, lane, &s_prev)) return;
+    if (wave < R) store_tile<1, 1>(v, reinterpret_cast<uint8_t*>(turn), a.resid, a.y, p.M, a.N, m0, n0 + 16 * wave, wave, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -480,7 +458,9 @@ struct MidLds {
     static constexpr int kQuad = kScaleWaves * 1024, kQuads = (S + 2) / 4 + 1, kBytes = kS + kQuads * kQuad;    // scales of 4 blocks per row
 };
 
-template <int BM, int BN, int WM, int WN, int S>
+// ANY: also takes tasks of fewer than four blocks, whose rows' scales do not
+// fill a 16-byte load; they go to registers before the first block.
+template <int BM, int BN, int WM, int WN, int S, bool ANY>
 __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s_prev) {
     using L = MidLds<BM, BN, S>;
     constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -512,11 +492,22 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     const int ks = p.ks[at.task];
     const int g0 = G * at.slice / ks, g1 = G * (at.slice + 1) / ks;      // (a slice has at least four blocks)
     auto quad_first = [&](int q) { return 4 * q + 4 <= g1 - g0 ? g0 + 4 * q : g1 - 4; };
+    const bool few = ANY && G < 4;
+    float fs[3][TM];
+    if (few) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(a.xs + (size_t)m0 * G, (uint32_t)rows_m * (uint32_t)G * 4u);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int u = 0; u < TM; ++u)
+                fs[i][u] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                         r, i < G ? ((wm * (BM / WM) + 16 * u + lr) * G + i) * 4 : (int)0xFFFFFFF0u, 0, 0));
+    }
     // block g0 + i into stage i % S; always kLoads loads, and those for the
     // scales before them, so that vmcnt counts blocks
     auto load = [&](int i, int stage) {
         const int g = g0 + i;
-        if (!(i & 3) && g < g1 && wave < L::kScaleWaves)
+        if (!few && !(i & 3) && g < g1 && wave < L::kScaleWaves)
             to_lds16(rs, soff, (uint32_t)quad_first(i >> 2) * 4, base + L::kS + (i >> 2) % L::kQuads * L::kQuad + wave * 1024);
         const uint32_t o = g >= g1 || (tail && g == G - 1 && 128u * g + chunk >= (uint32_t)K) ? 0xFFFF0000u : off;
 #pragma unroll
@@ -543,7 +534,7 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
         phase();
         const float s = next;
         if (g0 + i + 1 < g1) next = wsrow[g0 + i + 1];
-        const uint8_t* sc = lds + srow + (i >> 2) % L::kQuads * L::kQuad + (g0 + i - quad_first(i >> 2)) * 4;
+        const uint8_t* sc = lds + srow + (i >> 2) % L::kQuads * L::kQuad + (few ? 0 : g0 + i - quad_first(i >> 2)) * 4;
         u32x4 xf[TM][2], wf[TN][2];
         float f[TM];
 #pragma unroll
@@ -551,6 +542,7 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
             xf[u][0] = *reinterpret_cast<const u32x4*>(lds + xrow + stage * L::kXStage + u * 2048 + c0);
             xf[u][1] = *reinterpret_cast<const u32x4*>(lds + xrow + stage * L::kXStage + u * 2048 + c1);
             f[u] = *reinterpret_cast<const float*>(sc + u * 256);
+            if (few) f[u] = i == 0 ? fs[0][u] : i == 1 ? fs[1][u] : fs[2][u];
         }
 #pragma unroll
         for (int t = 0; t < TN; ++t) {
@@ -584,11 +576,11 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
     store_tile<TM, TN>(acc, lds, a.resid, a.y, p.M, a.N, m0 + wm * (BM / WM), n0 + wn * (BN / WN), wave, lane);
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int S, bool ANY>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_mid_kernel(Fp8Group p) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[MidLds<BM, BN, S>::kBytes];
     __shared__ unsigned s_prev;
-    mid<BM, BN, WM, WN, S>(p, lds, &s_prev);
+    mid<BM, BN, WM, WN, S, ANY>(p, lds, &s_prev);
 }
 
 // ---------------------------------------------------------------------------
@@ -612,27 +604,26 @@ struct Kind {
     hipError_t (*launch)(const Fp8Group&, dim3, hipStream_t);
 };
 
-template <int MT, int R>
+template <int R>
 hipError_t go_rows(const Fp8Group& p, dim3 g, hipStream_t s) {
-    return launch_kernel(fp8_rows_kernel<MT, R>, g, dim3(kWaves * 64), 0, s, p);
+    return launch_kernel(fp8_rows_kernel<R>, g, dim3(kWaves * 64), 0, s, p);
 }
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int S, bool ANY>
 hipError_t go_mid(const Fp8Group& p, dim3 g, hipStream_t s) {
-    return launch_kernel(fp8_mid_kernel<BM, BN, WM, WN, S>, g, dim3(64 * WM * WN), 0, s, p);
+    return launch_kernel(fp8_mid_kernel<BM, BN, WM, WN, S, ANY>, g, dim3(64 * WM * WN), 0, s, p);
 }
 template <int BM, int BN, int WM, int WN>
 hipError_t go_tile(const Fp8Group& p, dim3 g, hipStream_t s) {
     return launch_kernel(fp8_tile_kernel<BM, BN, WM, WN>, g, dim3(64 * WM * WN), 0, s, p);
 }
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int S, bool ANY = false>
 constexpr Kind mid_kind(int resident, float fixed, float b1, float b2 = 0, float b3 = 0, float b4 = 0) {
-    return Kind{BM, BN, WM * WN, (BM / WM / 16) * (BN / WN / 16), resident, fixed, {b1, b2, b3, b4}, 4, go_mid<BM, BN, WM, WN, S>};
+    return Kind{BM, BN, WM * WN, (BM / WM / 16) * (BN / WN / 16), resident, fixed, {b1, b2, b3, b4}, 4, go_mid<BM, BN, WM, WN, S, ANY>};
 }
 
-// few rows (no model: see plan_of), any M where a slice of K is short
-const Kind kRows16 = {16, 16, 1, 1, 1, 0, {}, 1, go_rows<1, 1>};
-const Kind kRows32 = {16, 32, 2, 1, 1, 0, {}, 1, go_rows<1, 2>};
-const Kind kRows64 = {64, 32, 8, 1, 1, 0, {}, 1, go_rows<4, 2>};
+// few rows (no model: see plan_of)
+const Kind kRows16 = {16, 16, 1, 1, 1, 0, {}, 1, go_rows<1>};
+const Kind kRows32 = {16, 32, 2, 1, 1, 0, {}, 1, go_rows<2>};
 const Kind kTiles[] = {
     mid_kind<32, 32, 2, 2, 4>(4, 3.5f, 0.20f, 0.30f, 0.42f, 0.55f),
     mid_kind<32, 64, 1, 4, 4>(3, 3.5f, 0.235f, 0.33f, 0.50f),
@@ -643,6 +634,13 @@ const Kind kTiles[] = {
     mid_kind<128, 128, 2, 2, 2>(2, 3.0f, 1.106f, 1.243f),
     mid_kind<256, 128, 4, 2, 3>(1, 6.5f, 1.13f),
     {256, 256, 8, 0, 1, 14.0f, {1.604f}, 4, go_tile<256, 256, 4, 2>},
+};
+// where a task has fewer than four blocks (4096 x 4096 x 384: 21 us; loaded
+// straight into registers, as few rows are, 106 us)
+const Kind kShortTiles[] = {
+    mid_kind<32, 64, 1, 4, 4, true>(3, 3.5f, 0.235f, 0.33f, 0.50f),
+    mid_kind<64, 64, 2, 2, 4, true>(2, 4.0f, 0.315f, 0.40f),
+    mid_kind<128, 128, 2, 2, 2, true>(2, 3.0f, 1.106f, 1.243f),
 };
 constexpr int kCUs = 256;
 constexpr int kMostSlices = 16;
@@ -724,12 +722,14 @@ Plan plan_of(const Fp8Args* t, int count, int M, size_t ws_bytes) {
         }
         return p;
     }
-    if (least < 4) {
-        p.kind = M <= 16 ? &kRows16 : &kRows64;
+    if (least < 4 && M <= 16) {
+        p.kind = &kRows16;
         return p;
     }
+    const Kind *kinds = least < 4 ? kShortTiles : kTiles, *end = least < 4 ? std::end(kShortTiles) : std::end(kTiles);
     double best = 0;
-    for (const Kind& k : kTiles) {
+    for (; kinds != end; ++kinds) {
+        const Kind& k = *kinds;
         int ks[kFp8MaxTasks];
         for (int i = 0; i < count; ++i) {
             ks[i] = 1;
@@ -771,23 +771,15 @@ hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, siz
     Plan plan = plan_of(tasks, count, M, ws ? kMostWs : 0);
     if (plan.ws > ws_bytes) plan = plan_of(tasks, count, M, 0);
     const Kind& k = *plan.kind;
-    // a grid holds fewer than 2^32 threads: more than that task by task, then in
-    // halves of the rows (one task that large has 512 rows and more, and no split)
+    // a grid holds fewer than 2^32 threads; eight tasks of few rows can have more
+    // (one has at most 2^20 workgroups of 512, and more rows have larger tiles:
+    // outputs of that many would not fit in memory)
     long groups = 0;
     for (int i = 0; i < count; ++i) groups += tiles_of(k, tasks[i].N, M) * plan.ks[i];
-    if (groups >= 1L << 23) {
+    if (count > 1 && groups >= 1L << 23) {
         for (int i = 0; i < count; ++i) {
-            const int rows = count > 1 ? M : (M / 2 + 255) & ~255;
-            for (int m0 = 0; m0 < M; m0 += rows) {
-                Fp8Args t = tasks[i];
-                const size_t at = (size_t)m0;
-                t.x += at * t.K;
-                t.xs += at * blocks_of(t.K);
-                if (t.resid) t.resid += at * t.N;
-                t.y += at * t.N;
-                const hipError_t e = launch_fp8_gemm(&t, 1, M - m0 < rows ? M - m0 : rows, ws, ws_bytes, s);
-                if (e != hipSuccess) return e;
-            }
+            const hipError_t e = launch_fp8_gemm(tasks + i, 1, M, ws, ws_bytes, s);
+            if (e != hipSuccess) return e;
         }
         return hipSuccess;
     }

@@ -352,8 +352,24 @@ def test_gemm_nan_stays_in_its_row_and_column(q4):
         assert torch.equal(y[~want], clean[~want])
 
 
-def test_gemm_past_one_grid(q4):
-    """More workgroups than one grid holds, outputs past 2^32 bytes and elements."""
+@pytest.mark.parametrize("M", [1, 16, 40, 200])
+def test_gemm_infinite_scale_stays_infinite(q4, M):
+    """An infinite weight scale in the last block: +-inf where that block's sum
+    is not zero, in its 128 weight rows only."""
+    for N, K in ((300, 128), (300, 640), (300, 2048)):
+        x, xs, w, ws = whole_operands(M, N, K, 80)
+        ws[1, -1] = float("inf")
+        y = q4.fp8b128_gemm(*to_gpu((x, xs, w, ws))).cpu().float()
+        last = x[:, -128:].float() @ w[128:256, -128:].float().T
+        want = torch.where(last == 0, torch.nan, torch.sign(last) * torch.inf)
+        assert torch.equal(torch.nan_to_num(y[:, 128:256], nan=1.0), torch.nan_to_num(want, nan=1.0)), (N, K)
+        ws[1, -1] = 1.0
+        clean = q4.fp8b128_gemm(*to_gpu((x, xs, w, ws))).cpu().float()
+        assert torch.equal(y[:, :128], clean[:, :128]) and torch.equal(y[:, 256:], clean[:, 256:])
+
+
+def test_gemm_past_32_bit_offsets(q4):
+    """Outputs past 2^32 bytes and elements."""
     M, N, K = 1 << 18, (1 << 16) + 1, 128
     print(f"gemm M={M} N={N} K={K}", flush=True)
     x, xs, w, ws = operands(4096, N, K, 60)
@@ -365,6 +381,36 @@ def test_gemm_past_one_grid(q4):
     ops = (xg[rows].cpu(), xsg[rows].cpu(), w, ws)
     check_gemm(y[rows], ops)
     del y, xg, xsg
+
+
+def test_group_past_one_grid(q4):
+    """Eight products with more workgroups together than one grid holds."""
+    M, N, K, part = 2, 1 << 24, 16, 4096
+    print(f"gemm group of 8, M={M} N={N} K={K}", flush=True)
+    x, xs, w, ws = operands(M, part, K, 61)
+    wg, wsg = gpu(w).repeat(N // part, 1), gpu(ws).repeat(N // part, 1)
+    scales = [gpu(xs) * (i + 1) for i in range(8)]
+    outs = q4.fp8b128_gemm_grouped([(gpu(x), s, wg, wsg, None, None) for s in scales])
+    for i, y in enumerate(outs):
+        for at in (0, N // 2, N - part):
+            check_gemm(y[:, at:at + part], (x, scales[i].cpu(), w, ws))
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 100, 16), (40, 300, 384), (64, 65, 128), (200, 1000, 272), (513, 2049, 256), (1000, 1030, 400)])
+def test_short_rows(q4, M, N, K):
+    """Fewer than four blocks, alone and beside a product of many."""
+    print(f"gemm M={M} N={N} K={K}", flush=True)
+    ops, other = operands(M, N, K, 70), operands(M, 200, 4096, 71)
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")
+    resid = torch.randn(M, N, generator=synth.make_gen(("short", M, N, K))).to(torch.bfloat16)
+    d, e = to_gpu(ops), to_gpu(other)
+    alone = q4.fp8b128_gemm(*d, residual=gpu(resid))
+    check_gemm(alone, ops, resid)
+    y, z = q4.fp8b128_gemm_grouped([(*d, gpu(resid), None), (*e, None, None)], workspace=ws)
+    check_gemm(y, ops, resid)
+    check_gemm(z, other)
+    whole = whole_operands(M, N, K, 72)
+    check_whole(q4.fp8b128_gemm(*to_gpu(whole)), whole)
 
 
 @pytest.mark.parametrize("M", [1, 16, 48, 100])
