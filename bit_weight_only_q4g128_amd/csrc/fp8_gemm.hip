@@ -77,23 +77,36 @@ __device__ __forceinline__ void store4(f32x4 o, const uint16_t* resid, uint16_t*
 // touches 16 rows with 8 bytes each; M = 240, N = 16385, K = 2048: 26.8 us so,
 // 19.1 us at N = 16384.)
 template <int W>
-__device__ __forceinline__ void store_rows(const f32x4* v, int stride, float* buf, const uint16_t* resid, uint16_t* y, int M, int N, int m,
-                                           int n, int lane) {
-    constexpr int kLanes = W < 64 ? W : 64, kRows = 64 / kLanes, kPitch = W + 4;
+struct RowOrder {
+    static constexpr int kEach = 16 * W / 64;      // elements of a lane, consecutive ones in consecutive lanes
+    static __device__ __forceinline__ int row(int i, int lane) { return W < 64 ? lane / W + 64 / W * i : i / (W / 64); }
+    static __device__ __forceinline__ int col(int i, int lane) { return W < 64 ? lane % W : lane + 64 * (i % (W / 64)); }
+};
+// The residual's elements, all on their way together (one by one, between the
+// stores: 3855 x 2311 x 256 48 us, so 26).
+template <int W>
+__device__ __forceinline__ void load_rows(const uint16_t* resid, int M, int N, int m, int n, int lane, uint16_t (&e)[RowOrder<W>::kEach]) {
+#pragma unroll
+    for (int i = 0; i < RowOrder<W>::kEach; ++i) {
+        const int r = m + RowOrder<W>::row(i, lane), c = n + RowOrder<W>::col(i, lane);
+        e[i] = resid[r < M && c < N ? (size_t)r * N + c : 0];
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_rows(const f32x4* v, int stride, float* buf, bool add, const uint16_t (&e)[RowOrder<W>::kEach],
+                                           uint16_t* y, int M, int N, int m, int n, int lane) {
+    constexpr int kPitch = W + 4;
     const int lr = lane & 15, lq = lane >> 4;
 #pragma unroll
     for (int t = 0; t < W / 16; ++t) *reinterpret_cast<f32x4*>(buf + lr * kPitch + 16 * t + 4 * lq) = v[t * stride];
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 4
-    for (int r = lane / kLanes; r < 16; r += kRows)
 #pragma unroll
-        for (int c = lane % kLanes; c < W; c += kLanes)
-            if (m + r < M && n + c < N) {
-                const size_t at = (size_t)(m + r) * N + n + c;
-                float o = buf[r * kPitch + c];
-                if (resid) o += __builtin_bit_cast(float, (uint32_t)resid[at] << 16);
-                y[at] = f32_to_bf16(o);
-            }
+    for (int i = 0; i < RowOrder<W>::kEach; ++i) {
+        const int r = RowOrder<W>::row(i, lane), c = RowOrder<W>::col(i, lane);
+        float o = buf[r * kPitch + c];
+        if (add) o += __builtin_bit_cast(float, (uint32_t)e[i] << 16);
+        if (m + r < M && n + c < N) y[(size_t)(m + r) * N + n + c] = f32_to_bf16(o);
+    }
     __builtin_amdgcn_wave_barrier();
 }
 
@@ -112,10 +125,15 @@ __device__ __forceinline__ void store_tile(const f32x4* v, uint8_t* lds, const u
                 if (m + 16 * u + lr < M && n + 16 * t + 4 * lq < N)
                     store4(v[t * TM + u], resid, y, N, m + 16 * u + lr, n + 16 * t + 4 * lq);
     } else {
-        float* buf = reinterpret_cast<float*>(lds) + wave * 16 * (16 * TN + 4);
+        constexpr int W = 16 * TN;
+        float* buf = reinterpret_cast<float*>(lds) + wave * 16 * (W + 4);
+        uint16_t e[2][RowOrder<W>::kEach];
+        if (resid) load_rows<W>(resid, M, N, m, n, lane, e[0]);
 #pragma unroll
-        for (int u = 0; u < TM; ++u)
-            if (m + 16 * u < M) store_rows<16 * TN>(v + u, TM, buf, resid, y, M, N, m + 16 * u, n, lane);
+        for (int u = 0; u < TM; ++u) {
+            if (resid && u + 1 < TM) load_rows<W>(resid, M, N, m + 16 * (u + 1), n, lane, e[(u + 1) & 1]);
+            if (m + 16 * u < M) store_rows<W>(v + u, TM, buf, resid != nullptr, e[u & 1], y, M, N, m + 16 * u, n, lane);
+        }
     }
 }
 
