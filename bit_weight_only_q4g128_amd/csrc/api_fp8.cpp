@@ -42,7 +42,7 @@ int check_group(const fp8b128_task* tasks, int count, int M, Fp8Args* a) {
         // a residual that is exactly this task's y is read before each element is written
         in[i][4] = t.residual && t.residual != t.y ? range_of(t.residual, ybytes) : Range{0, 0};
         out[i] = range_of(t.y, ybytes);
-        a[i] = Fp8Args{t.x, t.xscale, t.w, t.wscale, t.residual, t.y, t.N, t.K};
+        a[i] = Fp8Args{t.x, t.xscale, t.w, t.wscale, t.residual, t.y, t.N, t.K, t.N};
     }
     for (int i = 0; i < count; ++i)
         for (int j = 0; j < count; ++j) {

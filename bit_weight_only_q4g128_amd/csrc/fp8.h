@@ -17,6 +17,7 @@ struct Fp8Args {
     const uint16_t* resid;   // bf16 [M, N] or null; may equal y
     uint16_t* y;             // bf16 [M, N]
     int N, K;
+    int ld;                  // elements from a row of y and resid to the next
 };
 
 constexpr int kFp8Block = 128;    // columns (and weight rows) that share a scale

@@ -352,6 +352,31 @@ def test_gemm_nan_stays_in_its_row_and_column(q4):
         assert torch.equal(y[~want], clean[~want])
 
 
+@pytest.mark.parametrize("M,N,K", [(4096, 4097, 4096), (4000, 4100, 3600), (4096, 4360, 528)])
+def test_weight_rows_behind_the_last_tile(q4, M, N, K):
+    """Large products whose last weight rows go in a launch of their own."""
+    print(f"gemm M={M} N={N} K={K}", flush=True)
+    ops = whole_operands(M, N, K, 90)
+    rows = torch.tensor([0, 1, 255, 256, M // 2, M - 2, M - 1])
+    buf = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[32:32 + M * N].view(M, N)
+    d = to_gpu(ops)
+    q4.fp8b128_gemm(*d, out=y)
+    check_whole(y[rows], (ops[0][rows], ops[1][rows], *ops[2:]))
+    assert bool((buf[:32] == 7).all() and (buf[32 + M * N:] == 7).all())
+    # the rest from products of 16 rows at a time, another kernel
+    for m in range(0, M, 400):
+        part = q4.fp8b128_gemm(d[0][m:m + 16], d[1][m:m + 16], *d[2:])
+        assert torch.equal(part, y[m:m + 16])
+    r = torch.randint(-8, 9, (M, N), generator=synth.make_gen(("cut", M, N))).to(torch.bfloat16).cuda()
+    z = q4.fp8b128_gemm(*d, residual=r)
+    part = q4.fp8b128_gemm(d[0][-16:], d[1][-16:], *d[2:], residual=r[-16:])
+    assert torch.equal(part, z[-16:])
+    w = r.clone()
+    q4.fp8b128_gemm(*d, residual=w, out=w)
+    assert torch.equal(w, z)
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 200])
 def test_gemm_infinite_scale_stays_infinite(q4, M):
     """An infinite weight scale in the last block: +-inf where that block's sum
