@@ -131,6 +131,11 @@ class Fp8Task(ctypes.Structure):
     _fields_ = [("x", _p), ("xscale", _p), ("w", _p), ("wscale", _p), ("residual", _p), ("y", _p), ("N", _i), ("K", _i)]
 
 
+class Fp8Launch(ctypes.Structure):
+    """Mirror of the C struct fp8b128_launch."""
+    _fields_ = [("tile_m", _i), ("tile_n", _i), ("count", _i), ("N", _i * 8), ("slices", _i * 8), ("workspace_bytes", ctypes.c_size_t)]
+
+
 lib.fp8b128_quantize.argtypes = [_p, _p, _i, _i, _p, _p, _p]
 lib.fp8b128_quantize.restype = ctypes.c_int
 lib.fp8b128_gemm.argtypes = [_p, _p, _i, _i, _p, _p, _i, _p, _p, _p]
@@ -139,6 +144,8 @@ lib.fp8b128_gemm_grouped_ws.argtypes = [_p, _i, _i, _p, ctypes.c_size_t, _p]
 lib.fp8b128_gemm_grouped_ws.restype = ctypes.c_int
 lib.fp8b128_workspace_bytes.argtypes = [_p, _i, _i, ctypes.POINTER(ctypes.c_size_t)]
 lib.fp8b128_workspace_bytes.restype = ctypes.c_int
+lib.fp8b128_launches.argtypes = [_p, _i, _i, ctypes.c_size_t, _p, _i, ctypes.POINTER(_i)]
+lib.fp8b128_launches.restype = ctypes.c_int
 lib.q4_verify_topk.argtypes = [_p, _i, _i, _i, _p, _p, _p, _i, _p, _p, _f, _i, _p, _p, _p, _p, ctypes.c_size_t, _p]
 lib.q4_verify_topk.restype = ctypes.c_int
 lib.q4_verify_topk_workspace_bytes.argtypes = [_i, _i, _i, _i]
@@ -748,7 +755,8 @@ def fp8b128_gemm_grouped(items, workspace=None):
     w_scale fp32 [ceil(N / 128), ceil(K / 128)], residual and out bf16 [M, N]
     (out may be the residual).  workspace: optional uint8 device tensor of at
     least fp8b128_workspace_bytes(items) bytes, zero-filled before its first
-    use and reusable afterwards without clearing (lets few rows split K).
+    use and reusable afterwards without clearing (lets few rows split K; a
+    smaller one lets them less).
     Returns the list of outputs."""
     arr, count, outs, M, index = _fp8_task_array(items)
     _enqueue(index, lib.fp8b128_gemm_grouped_ws, arr, count, M, *_scratch(workspace, index))

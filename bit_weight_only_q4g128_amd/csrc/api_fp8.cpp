@@ -106,6 +106,15 @@ int fp8b128_workspace_bytes(const fp8b128_task* tasks, int count, int M, size_t*
     return Q4_OK;
 }
 
+int fp8b128_launches(const fp8b128_task* tasks, int count, int M, size_t workspace_bytes, fp8b128_launch* out, int most, int* launches) {
+    if (!launches || (most > 0 && !out)) return Q4_EINVAL_PTR;
+    Fp8Args a[q4::kFp8MaxTasks];
+    const int rc = check_group(tasks, count, M, a);
+    if (rc) return rc;
+    *launches = q4::fp8_gemm_launches(a, count, M, workspace_bytes, out, most);
+    return Q4_OK;
+}
+
 int fp8b128_gemm(const uint8_t* x, const float* xscale, int M, int K, const uint8_t* w, const float* wscale, int N,
                  const uint16_t* residual, uint16_t* y, void* stream) {
     const fp8b128_task t = {x, xscale, w, wscale, residual, y, N, K};

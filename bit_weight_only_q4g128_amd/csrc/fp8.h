@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "q4gemv.h"
+
 namespace q4 {
 
 // One product y = RN_bf16(sum_g xs[m, g] ws[n / 128, g] sum_k x[m, k] w[n, k] (+ resid)).
@@ -29,6 +31,10 @@ hipError_t launch_fp8_quantize(const uint16_t* x, const uint16_t* up, int M, int
 // Up to kFp8MaxTasks products of one batch size M.  ws: a workspace whose
 // first 64 KiB are arrival counters (zero, left zero), or null.
 hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, size_t ws_bytes, hipStream_t s);
+// The workspace with which a call has the launches that any larger one gives
+// it (0: none), and the launches that a call with ws_bytes has: how many, and
+// the first `most` of them into out.
 size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M);
+int fp8_gemm_launches(const Fp8Args* tasks, int count, int M, size_t ws_bytes, fp8b128_launch* out, int most);
 
 }  // namespace q4

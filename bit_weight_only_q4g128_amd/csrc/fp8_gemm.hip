@@ -783,46 +783,53 @@ constexpr int kCut = 256;      // weight rows of the largest tile
 // A split's workspace is at most this (a plan that wants more is not made).
 constexpr size_t kMostWs = 48u << 20;
 
-}  // namespace
+// A grid holds fewer than 2^32 threads; eight tasks of few rows can have more
+// (one has at most 2^20 workgroups of 512, and more rows have larger tiles:
+// outputs of that many would not fit in memory).
+bool one_grid(const Plan& p, const Fp8Args* t, int count, int M) {
+    long groups = 0;
+    for (int i = 0; i < count; ++i) groups += tiles_of(*p.kind, t[i].N, M) * p.ks[i];
+    return count == 1 || groups < 1L << 23;
+}
 
-size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) { return plan_of(tasks, count, M, kMostWs).ws; }
-
-hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, size_t ws_bytes, hipStream_t s) {
-    // (the plan does not depend on how much larger than needed the workspace is)
-    Plan plan = plan_of(tasks, count, M, ws ? kMostWs : 0);
-    if (plan.ws > ws_bytes) plan = plan_of(tasks, count, M, 0);
-    const Kind& k = *plan.kind;
+// Decides the launches of a call that may use ws_bytes of workspace and hands
+// them to f(plan, tasks, count), in order, until one fails.  Everything that
+// asks how a call runs (the launch, the workspace query) asks here.  A plan is
+// the best of those whose splits fit, so any workspace of at least the largest
+// plan.ws that kMostWs gives has the same launches as kMostWs.
+template <typename F>
+hipError_t each_launch(const Fp8Args* t, int count, int M, size_t ws_bytes, F&& f) {
+    if (ws_bytes > kMostWs) ws_bytes = kMostWs;
+    const Plan plan = plan_of(t, count, M, ws_bytes);
     // Weight rows behind the last whole 256 in a launch of their own, where the
     // model has both done sooner by more than a launch costs the host: a last
     // round that is nearly empty is left out (4096 x 4097 x 4096: 125 us in one,
     // 85 in two; 8192 x 8193 x 8192 511 and 460; but 4096 x 6000 x 4096 123 in
     // one).  Only where there are microseconds to plan in.
-    const Fp8Args& t = tasks[0];
-    if (count == 1 && plan.time > 40 && t.N > kCut && t.N % kCut) {
-        Fp8Args whole = t, rest = t;
-        whole.N = t.N - t.N % kCut;
-        rest.N = t.N % kCut;
-        rest.w += (size_t)whole.N * t.K;
-        rest.ws += (size_t)(whole.N / kFp8Block) * blocks_of(t.K);
+    if (count == 1 && plan.time > 40 && t->N > kCut && t->N % kCut) {
+        Fp8Args whole = *t, rest = *t;
+        whole.N = t->N - t->N % kCut;
+        rest.N = t->N % kCut;
+        rest.w += (size_t)whole.N * t->K;
+        rest.ws += (size_t)(whole.N / kFp8Block) * blocks_of(t->K);
         if (rest.resid) rest.resid += whole.N;
         rest.y += whole.N;
-        if (plan_of(&whole, 1, M, ws ? ws_bytes : 0).time + plan_of(&rest, 1, M, ws ? ws_bytes : 0).time + 3 < plan.time) {
-            const hipError_t e = launch_fp8_gemm(&whole, 1, M, ws, ws_bytes, s);
-            return e == hipSuccess ? launch_fp8_gemm(&rest, 1, M, ws, ws_bytes, s) : e;
+        const Plan first = plan_of(&whole, 1, M, ws_bytes), second = plan_of(&rest, 1, M, ws_bytes);
+        if (first.time + second.time + 3 < plan.time) {
+            const hipError_t e = f(first, &whole, 1);
+            return e == hipSuccess ? f(second, &rest, 1) : e;
         }
     }
-    // a grid holds fewer than 2^32 threads; eight tasks of few rows can have more
-    // (one has at most 2^20 workgroups of 512, and more rows have larger tiles:
-    // outputs of that many would not fit in memory)
-    long groups = 0;
-    for (int i = 0; i < count; ++i) groups += tiles_of(k, tasks[i].N, M) * plan.ks[i];
-    if (count > 1 && groups >= 1L << 23) {
-        for (int i = 0; i < count; ++i) {
-            const hipError_t e = launch_fp8_gemm(tasks + i, 1, M, ws, ws_bytes, s);
-            if (e != hipSuccess) return e;
-        }
-        return hipSuccess;
+    if (one_grid(plan, t, count, M)) return f(plan, t, count);
+    for (int i = 0; i < count; ++i) {
+        const hipError_t e = each_launch(t + i, 1, M, ws_bytes, f);
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
+}
+
+hipError_t launch_plan(const Plan& plan, const Fp8Args* tasks, int count, int M, void* ws, hipStream_t s) {
+    const Kind& k = *plan.kind;
     Fp8Group p{};
     p.count = count;
     p.M = M;
@@ -843,6 +850,43 @@ hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, siz
         }
     }
     return k.launch(p, dim3(p.first[count]), s);
+}
+
+}  // namespace
+
+size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) {
+    size_t most = 0;
+    each_launch(tasks, count, M, kMostWs, [&](const Plan& p, const Fp8Args*, int) {
+        most = p.ws > most ? p.ws : most;
+        return hipSuccess;
+    });
+    return most;
+}
+
+hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, size_t ws_bytes, hipStream_t s) {
+    return each_launch(tasks, count, M, ws ? ws_bytes : 0,
+                       [&](const Plan& p, const Fp8Args* t, int n) { return launch_plan(p, t, n, M, ws, s); });
+}
+
+int fp8_gemm_launches(const Fp8Args* tasks, int count, int M, size_t ws_bytes, fp8b128_launch* out, int most) {
+    int n = 0;
+    each_launch(tasks, count, M, ws_bytes, [&](const Plan& p, const Fp8Args* t, int c) {
+        if (n < most) {
+            fp8b128_launch& l = out[n];
+            l = fp8b128_launch{};
+            l.tile_m = p.kind->bm;
+            l.tile_n = p.kind->bn;
+            l.count = c;
+            l.workspace_bytes = p.ws;
+            for (int i = 0; i < c; ++i) {
+                l.N[i] = t[i].N;
+                l.slices[i] = p.ks[i];
+            }
+        }
+        ++n;
+        return hipSuccess;
+    });
+    return n;
 }
 
 }  // namespace q4

@@ -431,13 +431,15 @@ int fp8b128_gemm(const uint8_t* x, const float* xscale, int M, int K, const uint
 /*
  * Up to 8 independent products of one batch size M (the projections that read
  * one input, for instance), each under fp8b128_gemm's rules.  workspace:
- * optional device memory of at least fp8b128_workspace_bytes (0: none is
- * used), 256-byte aligned, apart from every argument, zero-filled before its
- * first use; its first 64 KiB are arrival counters that every call leaves at
- * zero, the rest is scratch, so it can be shared with the library's other
- * calls that take a workspace of this kind.  It lets few rows split K over
- * workgroups (summed in slice order); without one, or with a smaller one, the
- * call runs unsplit.  Calls that use one workspace must not overlap in time.
+ * optional device memory, 256-byte aligned, apart from every argument,
+ * zero-filled before its first use; its first 64 KiB are arrival counters that
+ * every call leaves at zero, the rest is scratch, so it can be shared with the
+ * library's other calls that take a workspace of this kind.  It lets few rows
+ * split K over workgroups (summed in slice order).  A call runs in the way that
+ * is modelled fastest among those that the workspace holds: with
+ * fp8b128_workspace_bytes (0: none is used) as with any larger one, with less
+ * in fewer slices, without one unsplit.  Calls that use one workspace must not
+ * overlap in time.
  */
 typedef struct fp8b128_task {
     const uint8_t* x;          /* e4m3 [M, K] */
@@ -452,6 +454,18 @@ typedef struct fp8b128_task {
 
 int fp8b128_gemm_grouped_ws(const fp8b128_task* tasks, int count, int M, void* workspace, size_t workspace_bytes, void* stream);
 int fp8b128_workspace_bytes(const fp8b128_task* tasks, int count, int M, size_t* bytes);
+
+/*
+ * Diagnostic: the kernel launches that a call with this many bytes of workspace
+ * makes (nothing is launched): how many, and the first `most` of them.
+ */
+typedef struct fp8b128_launch {
+    int tile_m, tile_n;        /* batch and weight rows of a workgroup */
+    int count;                 /* products in it */
+    int N[8], slices[8];       /* of each: weight rows, slices of K */
+    size_t workspace_bytes;    /* that it uses */
+} fp8b128_launch;
+int fp8b128_launches(const fp8b128_task* tasks, int count, int M, size_t workspace_bytes, fp8b128_launch* out, int most, int* launches);
 
 /*
  * Verification of drafted tokens (speculative decoding by rejection sampling,
