@@ -19,8 +19,10 @@
 //
 // Whole numbers come out, so every quantity that decides one (exponentials,
 // masses, running sums) is held in fp64, whose vector rate on this machine is
-// that of unpacked fp32; a token can differ from exact arithmetic only where a
-// uniform lies within about 1e-11 of a boundary.
+// that of unpacked fp32.  A probability is within about 5e-15 of its value, a
+// boundary of the acceptance or of a draw from p within 1e-14 of its place.  For
+// a draw from max(p - q, 0), whose total R shrinks as the draft nears the target,
+// that is 1e-14 / R.
 #include "internal.h"
 #include "topk.h"
 #include "verify.h"
@@ -32,23 +34,27 @@ namespace {
 constexpr int kThreads = 256;
 
 // 2^y for y >= -1000 (below, and for NaN: 2^-1000): y = n + f, |f| <= 1/2,
-// with n from the low word of y + 1.5 * 2^52, and 2^f by the polynomial of
-// degree 8 with the least largest relative error on the interval (8e-13,
-// fitted by reweighted least squares).  Conversions to integer and ldexp, which
-// run at a fraction of the fp64 rate, are not needed.
+// with n from the low word of y + 1.5 * 2^52, and 2^f by a polynomial of degree
+// 11 whose constant term is 1 (interpolated at Chebyshev nodes of the interval;
+// it is off by 2e-17, its fp64 evaluation by 1.3e-16, so that differences of
+// close probabilities keep what fp64 holds of them, and 2^0 is 1).  Conversions
+// to integer and ldexp, which run at a fraction of the fp64 rate, are not needed.
 __device__ __forceinline__ double exp2_raw(double y) {
     constexpr double kShift = 6755399441055744.0;
     y = __builtin_fmax(y, -1000.0);
     const double k = y + kShift, f = y - (k - kShift);
-    double p = 1.3175848283035606e-06;
-    p = __builtin_fma(p, f, 1.5309737450565635e-05);
-    p = __builtin_fma(p, f, 1.5403851794620636e-04);
-    p = __builtin_fma(p, f, 1.3333452062188023e-03);
-    p = __builtin_fma(p, f, 9.6181285427970660e-03);
-    p = __builtin_fma(p, f, 5.5504109393417454e-02);
-    p = __builtin_fma(p, f, 2.4022650698880670e-01);
-    p = __builtin_fma(p, f, 6.9314718054651500e-01);
-    p = __builtin_fma(p, f, 9.9999999999976290e-01);
+    double p = 4.4549605981865186e-10;
+    p = __builtin_fma(p, f, 7.0725859492692234e-09);
+    p = __builtin_fma(p, f, 1.0178062445845774e-07);
+    p = __builtin_fma(p, f, 1.3215442587921689e-06);
+    p = __builtin_fma(p, f, 1.5252733829836119e-05);
+    p = __builtin_fma(p, f, 1.5403530441736050e-04);
+    p = __builtin_fma(p, f, 1.3333558146416936e-03);
+    p = __builtin_fma(p, f, 9.6181291076068882e-03);
+    p = __builtin_fma(p, f, 5.5504108664821597e-02);
+    p = __builtin_fma(p, f, 2.4022650695910097e-01);
+    p = __builtin_fma(p, f, 6.9314718055994529e-01);
+    p = __builtin_fma(p, f, 1.0);
     // (in assembly: the compiler makes five instructions of this addition)
     uint2 w = __builtin_bit_cast(uint2, p);
     asm("v_lshl_add_u32 %0, %1, 20, %0" : "+v"(w.y) : "v"(__builtin_bit_cast(uint2, k).x));

@@ -497,7 +497,9 @@ int fp8b128_launches(const fp8b128_task* tasks, int count, int M, size_t workspa
  * not finite has no distribution: nothing stands against it, and the token
  * drawn from it is -1.  A drafted token outside [0, V) never stands.  Masses
  * and running sums are fp64: a result differs from exact arithmetic only where
- * a uniform lies within about 1e-11 of a boundary.
+ * a uniform lies within about 1e-14 of a boundary, or, for a draw from
+ * max(p - q, 0), within 1e-14 over that distribution's total (a draft close to
+ * the target leaves little).
  *
  * 1 <= D <= 63, B (D + 1) <= 65536; temperature finite and > 0.  Alignment:
  * logits 2 bytes, everything else 4.  workspace: at least
