@@ -704,7 +704,9 @@ __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int c
         const double own = use_rest ? rs : as;
         const double run = wave_scan(own), total = lane_value(run, 63);
         const double x = ru * total;
-        const unsigned long long over = __ballot(run > x), any = __ballot(own > 0.0);
+        // (own > 0: the lanes' prefix sums are rounded in different orders, so
+        // that of a lane without mass can exceed its neighbour's by a bit)
+        const unsigned long long over = __ballot(run > x && own > 0.0), any = __ballot(own > 0.0);
         const int l = over ? (int)__builtin_ctzll(over) : any ? 63 - (int)__builtin_clzll(any) : -1;
         if (l < 0) {
             if (lane == 0) s_chunk = -1;

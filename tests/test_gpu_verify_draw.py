@@ -86,3 +86,27 @@ def test_residual_draw_next_to_a_boundary(q4, V, T, values):
     token, count, _ = q4.verify_full(logits, draft, gpu(u), draft_logits=draft_logits, temperature=T)
     assert int(count.sum()) == 0                # (q > p and the largest u: refused)
     assert token[:, 0].tolist() == tokens
+
+
+def test_draw_next_to_a_masked_region(q4):
+    """Rows of equal logits whose masses before and behind a masked region are
+    equal, and a uniform of one half: the running sums over the empty region lie
+    within an fp64 rounding of the place that is sought.  The token is one of the
+    region's neighbours, and never -1 or a masked one."""
+    V, B = 16384, 400
+    rng = np.random.default_rng(0)
+    logits = np.full((B, 2, V), -np.inf, np.float32)
+    allowed = []
+    for b in range(B):
+        a, gap = int(rng.integers(2, 5)), int(rng.integers(1, 3))       # parts of 2048: before the region, the region
+        before = [2048 * c + rng.permutation(2048)[:rng.integers(1, 700)] for c in range(a)]
+        left = np.sort(np.concatenate(before))
+        right = 2048 * (a + gap) + np.sort(rng.permutation(V - 2048 * (a + gap))[:len(left)])
+        logits[b, 0, left] = logits[b, 0, right] = 1.0
+        allowed.append((int(left[-1]), int(right[0])))
+    logits[:, 1] = 0.0
+    token, count, _ = q4.verify_full(gpu(torch.from_numpy(logits).to(torch.bfloat16)), torch.zeros(B, 1, dtype=torch.int32, device="cuda"),
+                                     torch.full((B, 2), 0.5, device="cuda"), n_draft=torch.zeros(B, dtype=torch.int32, device="cuda"))
+    assert int(count.sum()) == 0
+    wrong = [(b, t, allowed[b]) for b, t in enumerate(token[:, 0].tolist()) if t not in allowed[b]]
+    assert not wrong, f"{len(wrong)} of {B}: {wrong[:5]}"
