@@ -38,7 +38,11 @@ __device__ __forceinline__ u32x4 ld16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
 // Loads straight to LDS, 16 or 4 bytes per lane in lane order from LDS address
 // `to` on.  Assembly, because around the builtin the compiler waits for every
 // such load before any read of LDS, also of another stage; the kernels below
-// wait by themselves (vmcnt, then a barrier).  Nothing is written to registers.
+// wait by themselves (vmcnt, then a barrier).  Nothing is written to registers;
+// the compiler puts `to` into m0 (a wait state before its use).  There is no
+// memory clobber, which would bring those waits back: that LDS is not read before
+// the load has ended, nor written while it is read, rests on the s_waitcnt and
+// phase() (a barrier across which nothing moves) around it.
 // The descriptor's check covers the sum of a lane's and the scalar offset and
 // does not wrap (measured with both past it): what lies behind gives zeros.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -47,7 +51,7 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes) {
     return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), (int)bytes, kBufferFlags};
 }
 __device__ __forceinline__ void to_lds16(i32x4 r, uint32_t off, uint32_t soff, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(r), "s"(soff), "s"(to));
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(r), "s"(soff), "{m0}"(to));
 }
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
@@ -856,7 +860,7 @@ hipError_t launch_plan(const Plan& plan, const Fp8Args* tasks, int count, int M,
 
 size_t fp8_gemm_ws_bytes(const Fp8Args* tasks, int count, int M) {
     size_t most = 0;
-    each_launch(tasks, count, M, kMostWs, [&](const Plan& p, const Fp8Args*, int) {
+    (void)each_launch(tasks, count, M, kMostWs, [&](const Plan& p, const Fp8Args*, int) {
         most = p.ws > most ? p.ws : most;
         return hipSuccess;
     });
@@ -870,7 +874,7 @@ hipError_t launch_fp8_gemm(const Fp8Args* tasks, int count, int M, void* ws, siz
 
 int fp8_gemm_launches(const Fp8Args* tasks, int count, int M, size_t ws_bytes, fp8b128_launch* out, int most) {
     int n = 0;
-    each_launch(tasks, count, M, ws_bytes, [&](const Plan& p, const Fp8Args* t, int c) {
+    (void)each_launch(tasks, count, M, ws_bytes, [&](const Plan& p, const Fp8Args* t, int c) {
         if (n < most) {
             fp8b128_launch& l = out[n];
             l = fp8b128_launch{};
