@@ -717,7 +717,12 @@ def fp8b128_quantize(x, up=None, codes=None, scale=None):
     return codes, scale
 
 
-def _fp8_task_array(items):
+_NO_OUTPUT = 1 << 60      # an address that no tensor has, and room for any output behind it
+
+
+def _fp8_task_array(items, sizing=False):
+    """The tasks' bytes, their count, the outputs, M and the device.  sizing: for
+    a question about sizes alone, outputs that are not given are not made."""
     items = list(items)
     count = len(items)
     if not 1 <= count <= 8:
@@ -738,12 +743,18 @@ def _fp8_task_array(items):
         if not isinstance(w, torch.Tensor) or w.dim() != 2:
             raise ValueError("w must be a tensor of 2 dims")
         N = w.shape[0]
-        y = x_scale.new_empty((M, N), dtype=torch.bfloat16) if out is None else out
+        if out is not None:
+            y, yp = out, _tensor(out, "out", _BF16, (M, N), index)
+        elif sizing:
+            y, yp = None, _NO_OUTPUT + (len(arr) << 50)
+        else:
+            y = x_scale.new_empty((M, N), dtype=torch.bfloat16)
+            yp = y.data_ptr()
         outs.append(y)
         arr.append(_FP8_TASK(xp, sp, _tensor(w, "w", _E4M3, (N, K), index),
                              _tensor(w_scale, "w_scale", _F32, ((N + _BLOCK - 1) // _BLOCK, G), index),
                              0 if residual is None else _tensor(residual, "residual", _U16, (M, N), index),
-                             y.data_ptr() if out is None else _tensor(y, "out", _BF16, (M, N), index), N, K))
+                             yp, N, K))
     return b"".join(arr), count, outs, M, index
 
 
@@ -765,7 +776,7 @@ def fp8b128_gemm_grouped(items, workspace=None):
 
 def fp8b128_workspace_bytes(items) -> int:
     """Bytes of workspace fp8b128_gemm_grouped can use for these items (0: none)."""
-    arr, count, _, M, _ = _fp8_task_array(items)
+    arr, count, _, M, _ = _fp8_task_array(items, sizing=True)
     n = ctypes.c_size_t(0)
     _raise(lib.fp8b128_workspace_bytes(arr, count, M, ctypes.byref(n)))
     return int(n.value)
