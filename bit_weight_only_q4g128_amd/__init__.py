@@ -677,6 +677,8 @@ def _optional(t, name: str, dtypes, shape, index: int):
 def _scratch(workspace, index: int):
     if workspace is None:
         return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace.data_ptr(), workspace.numel()

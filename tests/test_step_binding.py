@@ -34,3 +34,14 @@ def test_size_query_makes_no_outputs(monkeypatch):
     with pytest.raises(q4.Q4GemvError) as e:
         q4.fp8b128_workspace_bytes([(x, xs, w, ws, None, out), (x, xs, w, ws, None, out)])
     assert e.value.status == -4
+
+
+@pytest.mark.parametrize("workspace", [1 << 20, b"\0" * 256, "none", [0]])
+def test_workspace_that_is_no_tensor(monkeypatch, workspace):
+    """Refused as any other argument of a wrong type is."""
+    monkeypatch.setattr(q4, "_check", lambda *a: None)      # (host tensors stand for the GPU's)
+    lg, d, u = torch.zeros(1, 2, 8, dtype=torch.bfloat16), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2)
+    for call in (lambda: q4.fp8b128_gemm(*product(4, 256, 256), workspace=workspace),
+                 lambda: q4.verify_topk(lg, d, u, top_k=2, workspace=workspace), lambda: q4.verify_full(lg, d, u, workspace=workspace)):
+        with pytest.raises(TypeError, match="workspace"):
+            call()
