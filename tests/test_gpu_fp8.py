@@ -518,3 +518,21 @@ def test_binding_refusals(q4):
     assert e.value.status == -4
     torch.cuda.synchronize()
     assert bool((y == 3).all()), "a refused call wrote its output"
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 130])
+def test_group_gives_what_single_calls_give(q4, M):
+    """Each product of a group alone, bit for bit: operands whose sums are exact,
+    as a group and a single call can add K in different parts."""
+    tasks = [whole_operands(M, N, 2048, 100 + i) for i, N in enumerate((2048, 512, 515, 1030))] + [whole_operands(M, 300, 400, 110)]
+    tasks = [(tasks[0][0], tasks[0][1], *t[2:]) if t[0].shape[1] == 2048 else t for t in tasks]
+    d = [to_gpu(t) for t in tasks]
+    r = gpu(torch.randint(-8, 9, (M, 515), generator=synth.make_gen(("whole-r", M))).to(torch.bfloat16))
+    items = [(*t, r if i == 2 else None, None) for i, t in enumerate(d)]
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")
+    for work in (None, ws):
+        outs = q4.fp8b128_gemm_grouped(items, workspace=work)
+        for i, y in enumerate(outs):
+            assert torch.equal(y, q4.fp8b128_gemm(*d[i], residual=items[i][4], workspace=work)), i
+            if i != 2:
+                check_whole(y, tasks[i])
