@@ -574,6 +574,7 @@ __device__ __forceinline__ void mid(const Fp8Group& p, uint8_t* lds, unsigned* s
         }
         __builtin_amdgcn_sched_barrier(0);      // the reads are asked for before the next loads
         load(i + S - 1, ahead);
+        __builtin_amdgcn_sched_barrier(0);      // and none of these sinks behind the products
 #pragma unroll
         for (int u = 0; u < TM; ++u) f[u] *= s;
 #pragma unroll
