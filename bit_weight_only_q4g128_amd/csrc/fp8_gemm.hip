@@ -80,7 +80,7 @@ __device__ __forceinline__ void store4(f32x4 o, const uint16_t* resid, uint16_t*
 // address: through LDS (buf: 16 rows of W + 4 floats, the wave's own), so that
 // a store writes consecutive elements.  (Straight from the fragments a store
 // touches 16 rows with 8 bytes each; M = 240, N = 16385, K = 2048: 26.8 us so,
-// 19.1 us at N = 16384.)
+// 23 us through LDS.)
 template <int W>
 struct RowOrder {
     static constexpr int kEach = 16 * W / 64;      // elements of a lane, consecutive ones in consecutive lanes
@@ -213,7 +213,7 @@ __device__ __forceinline__ bool join(f32x4 (&v)[NF], const Fp8Group& p, const Wh
 // Few rows: a workgroup of eight waves owns 16 R weight rows and 16 batch rows
 // over a slice of K; the waves share the slice's blocks, each loading its
 // own fragments straight into registers, and meet in LDS.  Bound by the latency
-// of a launch and of one round of loads: 1 x 2048 x 8192 (M x N x K) 7.4 us for
+// of a launch and of one round of loads: 1 x 2048 x 8192 (M x N x K) 7.7 us for
 // 16.8 MB, 1 x 2048 x 2048 4.5 us; at 8 x 8192 x 8192 17 us, 3.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
@@ -291,7 +291,8 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
 // WM x WN waves, each BM / WM x BN / WN.  Per 128-column block the tile's rows
 // go straight from memory to LDS (16 bytes per lane, no registers), into one
 // of two stages: while the waves compute a block, the next one is on its way.
-// Bound by the matrix cores' power: 8192 x 8192 x 8192 455 us, 2410 TFLOP/s (the
+// Bound by the matrix cores' power: 8192 x 8192 x 8192 456 us a call in a stream of
+// calls, 2410 TFLOP/s (the
 // card lowers its clock to about 1.95 GHz under it; the matrix cores are then
 // busy for 60 to 65 % of the cycles, the rest being the folds and the reads of
 // LDS that do not overlap them, and the last round's tail).
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Group p) {
 // it takes.  Several workgroups share a CU and fill each other's waits; K may
 // be split over workgroups where the tiles alone are too few.  Bound by the
 // weights' bytes and the fill of the stages: 48 x (2048, 512, 512, 8192, 8192) x
-// 2048 13.5 us, 3.1 TB/s; 240 x 16385 x 2048 21 us; 240 x 2048 x 8192 14 us;
+// 2048 12.8 us, 3.3 TB/s; 240 x 16385 x 2048 22 us; 240 x 2048 x 8192 14 us;
 // 2048 x 2048 x 2048 16.5 us, 1040 TFLOP/s.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int S>
@@ -617,6 +618,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_mid_kernel(Fp8Group p) {
 // rate such launches reach, plus the hand-over of a split.  Small tiles fill
 // the CUs early, large ones move fewer bytes per product: at 240 x 8192 x 2048
 // 64 x 64 takes 11.4 us and 256 x 128 21 us, at 4096 x 2048 x 8192 151 and 81.
+// The model puts 240 x 16384 x 2048 at 16.6 us and 240 x 16385 x 2048 at 22.4, calls
+// in a stream take 17.1 and 22.3; M = 512, N = 8249 at 58.9 us (K = 7904), measured 59.7.
 // ---------------------------------------------------------------------------
 constexpr int kMaxResident = 4;
 struct Kind {

@@ -15,15 +15,19 @@
 // c = 448 / a held as c_hi (16 significant bits) + c_lo, x * c_hi is exact in
 // fp32 and fma(x, c_lo, x * c_hi) is the quotient times 1 + 2^-38, rounded
 // once: an exact tie stays exact, and quotients that are no tie differ from
-// one by at least 2^-13 of their value (an 11-bit by an 8-bit integer).
+// one by at least 2^-13 of their value (an 11-bit by an 8-bit integer).  A gated
+// h is an fp32 number a few ulps from silu(x) up, and its quotient rounds twice:
+// about one code in 10^6, whose quotient lies at a tie, is the other neighbour
+// than exact arithmetic's (8192 x 8192: 74 to 94 codes of 67 million; the formula in
+// fp32 operations 78 to 93, so the fp32 h is the limit).
 //
 // Bound by memory: 3 bytes per value and 4 per block (5 per value gated).
 // Sixteen lanes hold one block (8 columns each, one 16-byte load), a wave four
 // blocks of a row; the largest value meets in four DPP steps, so that a value is
 // read once and nothing passes through LDS.  Waves are short and many: enough
 // loads are in flight without more than one unit per wave.  8192 x 8192 gated:
-// 62 us, 5.4 TB/s (a large copy reaches 5.1 TB/s); 4099 x 2000: 6 us, 4.1 TB/s,
-// from the cache behind L2; 240 x 8192 gated 4.3 us and one row of 2048 1.5 us,
+// 64 us, 5.3 TB/s (a large copy reaches 5.1 TB/s); 4099 x 2000: 6.1 us, 4.1 TB/s,
+// from the cache behind L2; 240 x 8192 gated 4.2 us and one row of 2048 1.6 us,
 // a launch's own time.
 #include "fp8.h"
 #include "internal.h"

@@ -132,9 +132,9 @@ __device__ __forceinline__ float accept_ratio(double p, double q) {
 //
 // Bound by latency and, for many rows, by the selection's instructions (about
 // 550 per wave and block, half of them two sorts of 64), not by the 2 bytes per
-// logit: one sequence with 4 drafted tokens, V = 2049, k = 30: 7.6 us, of which a
-// launch is 1.5 and the logits' round trip about 2; 48 sequences, V = 16385: 8.6
-// and 5.1 us.  Two waves share a row above 512 logits or candidates: V = 2049 in
+// logit: one sequence with 4 drafted tokens, V = 2049, k = 30: 7.8 us, of which a
+// launch is 1.5 and the logits' round trip about 2; 48 sequences, V = 16385: 9.0
+// and 5.3 us.  Two waves share a row above 512 logits or candidates: V = 2049 in
 // a graph 9.3 us, one wave with 40 logits per lane 12.5; V = 300 5.2 us in one.
 // ---------------------------------------------------------------------------
 constexpr int kRowsAtOnce = 8;                      // of a workgroup of the last launch
@@ -293,11 +293,11 @@ __global__ __launch_bounds__(kRowsAtOnce * W * 64) void verify_topk_kernel(Verif
 // launch: the sums of max(p - q, 0) and of p over the chunks of each sequence's
 // stop row; the last one finds the chunk, then the entry, that the draw hits.
 //
-// Few sequences are bound by latency: one with 4 drafted tokens, V = 16385: 5.9
-// and 6.0 us, each a launch, one round of loads, the arrival (about 2 us) and
+// Few sequences are bound by latency: one with 4 drafted tokens, V = 16385: 6.5
+// and 7.3 us, each a launch, one round of loads, the arrival (about 2 us) and
 // what the last workgroup does alone.  Many are bound by memory, and that at the
-// ends: 32 with 7, V = 131072: 33 us for 101 to 126 MB, then 16 us, of which the
-// stop rows' 15 MB are about 5.
+// ends: 32 with 7, V = 131072: 34.6 us for 101 to 126 MB, then 18.6 us, of which the
+// stop rows' 15 MB are about 5 and the exponentials' arithmetic about half.
 //
 // A row starts at any even address.  It is read as the 16-byte aligned groups
 // of 8 logits that touch it; the first and the last, where the row ends inside
@@ -523,11 +523,11 @@ __global__ __launch_bounds__(kThreads) void row_mass_kernel(VerifyArgs a, int ro
 // and the sum does not depend on the order of the additions to them).  Other
 // values, rare in logits, are added one by one; -inf and NaN not at all.
 // An exponential per logit is bound by the fp64 arithmetic: 32 sequences with 7
-// drafted tokens and V = 131072, both launches, 67 us against 53 us, 128 with 4
-// and V = 32768 54 against 49.  It stays the better one below that (128 with 4,
-// V = 8192: 23 against 27 us), and for rows of other logits: nearly all of them
-// the type's lowest value or zero 66 against 90 us, all the same value 65
-// against 190 (the bin's additions wait for each other).
+// drafted tokens and V = 131072, both launches, 79 us against 55 us, 128 with 4
+// and V = 32768 55 against 51.  It stays the better one below that (128 with 4,
+// V = 8192: 22 against 26 us), and for rows of other logits: nearly all of them
+// the type's lowest value 74 against 103 us, all the same value 65 against 244
+// (the bin's additions wait for each other).
 constexpr int kHistJ = 32;                              // most groups per thread
 constexpr int kHistStep = 4;                            // of them at a time
 constexpr uint32_t kBinLow = 0x3980, kBins = 18 * 128;  // bits of 2^-12; bins of one sign
@@ -659,7 +659,8 @@ __device__ __forceinline__ void stop_values(const VerifyArgs& a, const Row& tr, 
 }
 
 // Block (b, chunk); a chunk is a group per thread (two and four were no faster
-// anywhere: 32 sequences with V = 131072 51 us, 53 and 54 with the first launch).
+// anywhere: 32 sequences with V = 131072, with the first launch and an exponential
+// of three terms less, 51 us, 53 and 54).
 __global__ __launch_bounds__(kThreads) void stop_draw_kernel(VerifyArgs a, int chunks, double c, const Stop* stop, unsigned* cnt, Part* parts) {
     __shared__ double s_wave[2][4];
     __shared__ unsigned s_prev;

@@ -419,7 +419,9 @@ int bf16_head_sample_ws(const uint16_t* x, int M, int K, const uint16_t* w, int 
  * taken as 0 for g below -87.3), x and up bf16 [M, K].  With a the largest |h|
  * of a block of 128 columns:
  *     scale[m, g] = RN(a / 448),  codes[m, k] = RN_e4m3(h[m, k] * 448 / a),
- * the quotient rounded once (exactly so without up); nothing saturates.  A
+ * the quotient rounded once (exactly so without up; with up, h and its quotient
+ * carry fp32 roundings, and about one code in 10^6 lies so near a tie that it
+ * goes the other way than in exact arithmetic); nothing saturates.  A
  * block of zeros has scale 0 and codes 0.  A value that is not finite (x, or
  * x * up in fp32) gets the NaN code and takes no part in a.
  */
