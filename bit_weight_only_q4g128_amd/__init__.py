@@ -20,6 +20,7 @@ __all__ = [
     "q4g128_gemv_fused", "q4g128_fused_workspace_bytes", "sample_topk", "bf16_head_sample", "bf16_head_sample_workspace_bytes", "q4g128_gemm", "gemv_grouped_mixed", "mixed_workspace_bytes",
     "fp8b128_quantize", "fp8b128_gemm", "fp8b128_gemm_grouped", "fp8b128_workspace_bytes",
     "verify_topk", "verify_topk_workspace_bytes", "verify_full", "verify_full_workspace_bytes",
+    "rope_cache", "attention_decode", "attention_decode_workspace_bytes", "attention_prefill",
     "variant_name", "strerror", "Q4GemvError", "LIB_PATH", "lib", "stream_read", "stream_read_sink_words",
     "VARIANT_AUTO", "VARIANT_DOT2", "VARIANT_MFMA", "VARIANT_STREAM", "VARIANT_TILED", "VARIANT_GEMM", "FMT_Q4G128", "FMT_NVFP4G16", "FMT_BF16",
 ]
@@ -154,6 +155,15 @@ lib.q4_verify_full.argtypes = [_p, _i, _i, _i, _p, _p, _p, _p, _f, _p, _p, _p, _
 lib.q4_verify_full.restype = ctypes.c_int
 lib.q4_verify_full_workspace_bytes.argtypes = [_i, _i, _i]
 lib.q4_verify_full_workspace_bytes.restype = ctypes.c_size_t
+_l = ctypes.c_int64
+lib.q4_rope_cache.argtypes = [_p, _p, _p, _i, _i, _i, _i, _l, _l, _l, _p, _p, _f, _p, _p, _i, _i, _p, _p, _p, _p, _p]
+lib.q4_rope_cache.restype = ctypes.c_int
+lib.q4_attention_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
+lib.q4_attention_decode_workspace_bytes.restype = ctypes.c_size_t
+lib.q4_attention_decode.argtypes = [_p, _i, _i, _i, _i, _i, _l, _p, _p, _i, _p, _p, _f, _i, _p, _p, ctypes.c_size_t, _p]
+lib.q4_attention_decode.restype = ctypes.c_int
+lib.q4_attention_prefill.argtypes = [_p, _i, _p, _p, _i, _i, _i, _i, _l, _l, _l, _p, _p, _i, _f, _i, _p, _p]
+lib.q4_attention_prefill.restype = ctypes.c_int
 
 
 class Q4GemvError(ValueError):
@@ -852,3 +862,177 @@ def verify_full(logits, draft, u, draft_logits=None, n_draft=None, temperature: 
              up, temperature, token.data_ptr(), count.data_ptr(), prob.data_ptr(),
              *_scratch(workspace, index))
     return token, count, prob
+
+
+# ---------------------------------------------------------------------------
+# A decoder layer's attention.  As above, another device may be current.
+# ---------------------------------------------------------------------------
+class KvCache(ctypes.Structure):
+    """Mirror of the C struct q4_kv_cache (an object of it, or its bytes)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("pages", _i), ("page_size", _i)]
+
+
+_KV_CACHE = struct.Struct("4Q2i").pack      # a KvCache's bytes
+assert ctypes.sizeof(KvCache) == 40
+_SLOT = (torch.int64,)
+
+
+def _heads(t, name: str, index: int, tokens=None, heads=None, D=None) -> int:
+    """Elements from a token of bf16 heads [tokens, heads, D] to the next; a
+    token's heads follow each other."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _U16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_U16}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got shape {tuple(t.shape)}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{index}" if index >= 0 else "a GPU"))
+    n, h, d = t.shape
+    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (D is not None and d != D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens or n, heads or h, D or d)}")
+    stride, of_head, one = t.stride()
+    if one != 1 or (of_head != d and h > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return stride if n > 1 else h * d
+
+
+def _kv_cache(cache, index: int, Hk: int, D: int):
+    """The C struct's bytes of (k, v) or (k, v, k_scale, v_scale), and the page size."""
+    cache = tuple(cache)
+    if len(cache) not in (2, 4):
+        raise ValueError("cache must be (k, v) or (k, v, k_scale, v_scale)")
+    k, v = cache[:2]
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.shape[1] != Hk or k.shape[3] != D:
+        raise ValueError(f"cache: k must be a tensor [pages, {Hk}, page_size, {D}]")
+    pages, _, page_size, _ = k.shape
+    types = _E4M3 if len(cache) == 4 else _U16
+    kp, vp = _tensor(k, "cache: k", types, k.shape, index), _tensor(v, "cache: v", types, k.shape, index)
+    ksp = vsp = 0
+    if len(cache) == 4:
+        shape = (pages, Hk, page_size)
+        ksp, vsp = _tensor(cache[2], "cache: k_scale", _F32, shape, index), _tensor(cache[3], "cache: v_scale", _F32, shape, index)
+    return _KV_CACHE(kp, vp, ksp, vsp, pages, page_size), page_size
+
+
+def rope_cache(q, k, v=None, positions=None, inv_freq=None, q_norm=None, k_norm=None, eps: float = 1e-6, interleaved: bool = False,
+               cache=None, slots=None, q_out=None, k_out=None):
+    """q's and k's heads normalised (q_norm, k_norm: bf16 weights [D], or None)
+    and rotated (positions int32 [T], inv_freq fp32 [rot / 2], None: no
+    rotation), and k and v appended to a paged cache (q4_rope_cache in the C
+    header).  q bf16 [T, Hq, D], k and v [T, Hk, D]; their tokens may lie
+    apart, as parts of one product's rows do.  cache: (k, v) bf16
+    [pages, Hk, page_size, D], or (k, v, k_scale, v_scale) with e4m3 codes and
+    fp32 scales [pages, Hk, page_size]; slots int64 [T]: page * page_size +
+    place of each token, -1 to not keep it.  q_out: a tensor to write into (q
+    itself: in place); k_out the same, True for a new one, None for none (a new
+    one without a cache).  Returns (q_out, k_out)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    index = q.get_device()
+    qs = _heads(q, "q", index)
+    T, Hq, D = q.shape
+    ks = _heads(k, "k", index, T, None, D)
+    Hk = k.shape[1]
+    vs, rot, vp, sp, cp = Hk * D, 0, None, None, None
+    if cache is not None:
+        vs, vp = _heads(v, "v", index, T, Hk, D), v.data_ptr()
+        sp = _tensor(slots, "slots", _SLOT, (T,), index)
+        cp, _ = _kv_cache(cache, index, Hk, D)
+    elif v is not None or slots is not None:
+        raise ValueError("v and slots are of a cache, and there is none")
+    pp = fp = None
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a tensor of 1 dim")
+        rot = 2 * inv_freq.shape[0]
+        fp, pp = _tensor(inv_freq, "inv_freq", _F32, inv_freq.shape, index), _tensor(positions, "positions", _I32, (T,), index)
+    if q_out is None:
+        q_out = q.new_empty((T, Hq, D))
+    elif q_out is not q:
+        _tensor(q_out, "q_out", _U16, (T, Hq, D), index)
+    if k_out is True or (k_out is None and cache is None):
+        k_out = k.new_empty((T, Hk, D))
+    elif k_out is not None and k_out is not k:
+        _tensor(k_out, "k_out", _U16, (T, Hk, D), index)
+    _enqueue(index, lib.q4_rope_cache, q.data_ptr(), k.data_ptr(), vp, T, Hq, Hk, D, qs, ks, vs,
+             _optional(q_norm, "q_norm", _U16, (D,), index), _optional(k_norm, "k_norm", _U16, (D,), index), eps, pp, fp, rot,
+             1 if interleaved else 0, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), cp, sp)
+    return q_out, k_out
+
+
+def attention_decode_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
+    """Bytes of workspace attention_decode uses for T new tokens a sequence."""
+    return int(lib.q4_attention_decode_workspace_bytes(T, Hq, Hk, D))
+
+
+def attention_decode(q, cache, table, lengths, n_new=None, scale=None, window: int = 0, out=None, workspace=None):
+    """Attention of new tokens over a paged cache that already holds them
+    (q4_attention_decode in the C header): q bf16 [B, T, Hq, D], cache as for
+    rope_cache, table int32 [B, width] of page numbers (-1: none), lengths int32
+    [B] with the new tokens, n_new int32 [B] (None: T each), scale (None:
+    D ** -0.5), window (0: all keys).  workspace: uint8, at least
+    attention_decode_workspace_bytes, zero-filled before its first use and
+    reusable afterwards without clearing (None: one is made for the call).
+    Returns bf16 [B, T, Hq, D]; rows that see no key are 0."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 4:
+        raise ValueError(f"q must have 4 dims, got shape {tuple(q.shape)}")
+    index = q.get_device()
+    B, T, Hq, D = q.shape
+    if q.is_contiguous():
+        if index < 0 or q.dtype not in _U16:
+            _heads(q.view(B * T, Hq, D), "q", index)
+        stride = Hq * D
+    else:
+        if B > 1 and T > 1 and q.stride(0) != T * q.stride(1):
+            raise ValueError("q: rows of all tokens must lie equally far apart")
+        stride = _heads(q[:, 0] if T == 1 else q[0] if B == 1 else q.flatten(0, 1), "q", index)
+    if not isinstance(cache[0], torch.Tensor) or cache[0].dim() != 4:
+        raise ValueError("cache: k must be a tensor of 4 dims")
+    Hk = cache[0].shape[1]
+    cp, _ = _kv_cache(cache, index, Hk, D)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a tensor of 2 dims")
+    width = table.shape[1]
+    tp, lp = _tensor(table, "table", _I32, (B, width), index), _tensor(lengths, "lengths", _I32, (B,), index)
+    if workspace is None:
+        workspace = q.new_zeros(attention_decode_workspace_bytes(T, Hq, Hk, D), dtype=torch.uint8)
+    if out is None:
+        out = q.new_empty((B, T, Hq, D))
+    else:
+        _tensor(out, "out", _U16, (B, T, Hq, D), index)
+    _enqueue(index, lib.q4_attention_decode, q.data_ptr(), B, T, Hq, Hk, D, stride, cp, tp, width, lp,
+             _optional(n_new, "n_new", _I32, (B,), index), D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+             *_scratch(workspace, index))
+    return out
+
+
+def attention_prefill(q, k, v, starts, key_starts=None, scale=None, window: int = 0, out=None):
+    """Causal attention over packed prompts (q4_attention_prefill in the C
+    header): q bf16 [T, Hq, D], k and v [S, Hk, D] (tokens may lie apart),
+    sequence b's tokens rows starts[b] .. starts[b + 1] of q, its keys rows
+    key_starts[b] .. key_starts[b + 1] of k and v (None: starts, S = T); int32
+    [B + 1].  The last token sees the last key.  scale and window as for
+    attention_decode.  Returns bf16 [T, Hq, D]; rows of no sequence are not
+    written."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    index = q.get_device()
+    qs = _heads(q, "q", index)
+    T, Hq, D = q.shape
+    ks = _heads(k, "k", index, T if key_starts is None else None, None, D)
+    S, Hk, _ = k.shape
+    vs = _heads(v, "v", index, S, Hk, D)
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1:
+        raise ValueError("starts must be a tensor of 1 dim")
+    n = starts.shape[0]
+    sp, kp = _tensor(starts, "starts", _I32, (n,), index), _optional(key_starts, "key_starts", _I32, (n,), index)
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+    else:
+        _tensor(out, "out", _U16, (T, Hq, D), index)
+    _enqueue(index, lib.q4_attention_prefill, q.data_ptr(), T, k.data_ptr(), v.data_ptr(), S, Hq, Hk, D, qs, ks, vs, sp, kp, n - 1,
+             D ** -0.5 if scale is None else scale, window, out.data_ptr())
+    return out

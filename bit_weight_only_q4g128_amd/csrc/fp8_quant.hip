@@ -10,13 +10,8 @@
 // scale 0 and codes 0; a value that is not finite (x, or x * up in fp32) gets
 // the NaN code.
 //
-// The quotient h * 448 / a must round once: for bf16 x it often is an exact
-// tie of e4m3, which a quotient off by one fp32 ulp would break.  With
-// c = 448 / a held as c_hi (16 significant bits) + c_lo, x * c_hi is exact in
-// fp32 and fma(x, c_lo, x * c_hi) is the quotient times 1 + 2^-38, rounded
-// once: an exact tie stays exact, and quotients that are no tie differ from
-// one by at least 2^-13 of their value (an 11-bit by an 8-bit integer).  A gated
-// h is an fp32 number a few ulps from silu(x) up, and its quotient rounds twice:
+// The rounding is fp8_codes.h's: the quotient rounds once where h is a bf16
+// value.  A gated h is an fp32 number a few ulps from silu(x) up, and its quotient rounds twice:
 // about one code in 10^6, whose quotient lies at a tie, is the other neighbour
 // than exact arithmetic's (8192 x 8192: 74 to 94 codes of 67 million; the formula in
 // fp32 operations 78 to 93, so the fp32 h is the limit).
@@ -30,6 +25,7 @@
 // from the cache behind L2; 240 x 8192 gated 4.2 us and one row of 2048 1.6 us,
 // a launch's own time.
 #include "fp8.h"
+#include "fp8_codes.h"
 #include "internal.h"
 
 namespace q4 {
@@ -38,16 +34,6 @@ namespace {
 
 constexpr int kThreads = 256;
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-    return v > o ? v : o;
-}
-// largest of the 16 lanes of a DPP row
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-    return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(v))));
-}
 
 __device__ __forceinline__ uint32_t pk_abs_max(uint32_t a, uint32_t b) {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a & 0x7FFF7FFFu),
@@ -115,40 +101,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __re
         const uint32_t hi = p & 0xFFFF0000u, lo = p << 16;
         top = hi > lo ? hi : lo;
     }
-    top = row_max(top);
-    float a = __builtin_bit_cast(float, top);
-    float s = a;
-    // rare: a value that is not finite, or a block so small or large that
-    // 1 / a leaves the normal range (scaled by 2^64 or 2^-64, exactly)
-    if (__any(!(a < 0x1p100f) || (a < 0x1p-100f && top != 0))) {
-        top = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float v = h[k];
-            const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
-            if (b >= 0x7F800000u) h[k] = __builtin_nanf("");
-            else top = b > top ? b : top;
-        }
-        top = row_max(top);
-        s = __builtin_bit_cast(float, top);
-        const float f = s < 0x1p-100f ? 0x1p64f : s > 0x1p100f ? 0x1p-64f : 1.0f;
-        a = s * f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] *= f;
-    }
-    const float r = __builtin_amdgcn_rcpf(a);
-    float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, 448.0f * r) & 0xFFFFFF00u);
-    float lo = __builtin_fmaf(-hi, a, 448.0f) * r;
-    if (top == 0) hi = lo = 0.0f;
-    float c[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = __builtin_fmaf(h[k], lo, h[k] * hi);
-    int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
-    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w0, true);
-    int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
-    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], w1, true);
-    if (in) *reinterpret_cast<uint2*>(codes + at) = make_uint2((uint32_t)w0, (uint32_t)w1);
-    if (j == 0 && blk < G) scale[(size_t)m * G + blk] = s / 448.0f;
+    const Codes8 e = e4m3_codes<16>(h, lanes_max<16>(top));
+    if (in) *reinterpret_cast<uint2*>(codes + at) = e.codes;
+    if (j == 0 && blk < G) scale[(size_t)m * G + blk] = e.scale;
 }
 
 template <bool GATED>

@@ -524,6 +524,111 @@ int q4_verify_full(const uint16_t* logits, int B, int D, int V, const int32_t* d
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A decoder layer's attention: what lies between its q, k, v projections and
+ * its o projection.  The Rumik TTS Fast Inference post fuses "rotary position,
+ * cache" operations ("What Made It Faster"), the rumik-oss-1-int4 card's engine
+ * lists flash-decoding attention ("Running it").
+ *
+ * Heads have D = 64 or 128 values; Hq query heads share Hk key heads, query
+ * head h with key head h / (Hq / Hk).  Arrays of heads are bf16
+ * [tokens, heads, D] whose tokens lie `stride` elements apart (at least
+ * heads * D, a multiple of 8), so that they may be parts of one product's rows.
+ *
+ * The cache is paged: pages of page_size tokens (16, 32, 64, 128 or 256), each
+ * head's part of a page in one piece.  bf16, or, where scales are given,
+ * float8_e4m3fn codes with one fp32 scale per token and head
+ * (value = code * scale).
+ */
+typedef struct q4_kv_cache {
+    void* k;              /* bf16 or e4m3 [pages, Hk, page_size, D], 16-byte aligned */
+    void* v;              /* as k */
+    float* k_scale;       /* NULL, or fp32 [pages, Hk, page_size], 16-byte aligned */
+    float* v_scale;       /* as k_scale; both or neither */
+    int pages;
+    int page_size;
+} q4_kv_cache;
+
+/*
+ * Heads of q and k normalised, rotated to their positions, and k and v
+ * appended to a cache; for prompts and decode steps alike (T tokens).
+ * Per head x of q and k, in fp32, rounded once:
+ *     h = x * w / sqrt(mean(x^2) + eps),  w = q_norm or k_norm, bf16 [D] (NULL: h = x)
+ *     the first rot values of h in pairs (a, b), pair i turned by
+ *     f = positions[t] * inv_freq[i]:  (a cos f - b sin f, b cos f + a sin f);
+ *     pairs are elements (i, i + rot / 2), or (2 i, 2 i + 1) where interleaved
+ * rot: a multiple of 16, 0 to D (0: no rotation, positions and inv_freq are not
+ * used).  inv_freq fp32 [rot / 2]; angles are taken in fp64, whatever the
+ * position (int32 [T]).
+ * q_out: bf16 [T, Hq, D], or q itself (in place, with q's stride).  k_out: the
+ * same for k, or NULL where there is a cache.
+ * cache (NULL: none): token t's k and v go to slot slots[t] = page * page_size +
+ * place (int64 [T]); a token whose slot is no slot of the cache (-1, say) is not
+ * kept.  An e4m3 cache takes the unrounded h and v, with a the largest
+ * finite |h| of the head: scale = RN(a / 448), code = RN_e4m3(h * 448 / a); a
+ * value that is not finite becomes the NaN code.  Slots must differ: of a
+ * slot named twice the contents are not specified (nothing else is touched).
+ *
+ * 1 <= T <= 2^22, Hq and Hk 1 to 256, eps finite and > 0.  Alignment: arrays of
+ * heads and norm weights 16 bytes, positions and inv_freq 4, slots 8.  No
+ * output may overlap an input or another output but in place as said.
+ */
+int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T, int Hq, int Hk, int D, int64_t q_stride,
+                  int64_t k_stride, int64_t v_stride, const uint16_t* q_norm, const uint16_t* k_norm, float eps,
+                  const int32_t* positions, const float* inv_freq, int rot, int interleaved, uint16_t* q_out, uint16_t* k_out,
+                  const q4_kv_cache* cache, const int64_t* slots, void* stream);
+
+/*
+ * Attention of new tokens over a paged cache that already holds them:
+ *     y[b, i, h] = RN_bf16( sum_j p_j v_j ),  p = softmax over the seen keys j of scale * q[b, i, h] . k_j
+ * T = 1: a decode step; T > 1: the rows that verify drafted tokens (q4_verify_*),
+ * of which sequence b has n = n_new[b] (NULL: T each; taken within 0 .. T).
+ * lengths[b] (int32): the sequence's tokens in the cache, the new ones the last
+ * of them; row i sees the first lengths[b] - n + i + 1, and of those the last
+ * `window` (0: all).  table int32 [B, width]: page numbers, token j on page
+ * table[b, j / page_size]; an entry that is no page of the cache (-1, say)
+ * holds nothing, and its tokens are not seen.  Lengths are taken within
+ * 0 .. width * page_size; nothing behind a sequence's length is read.
+ * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
+ * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
+ * Keys and values that a row does not see have no effect on it, whatever they
+ * hold.  Softmax and sums are fp32; a weight (times an 8-bit value's scale) is
+ * rounded to bf16 before it multiplies its value.
+ *
+ * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
+ * 2^24; scale finite and > 0; window >= 0.  Alignment: q and y 16 bytes, table,
+ * lengths, n_new 4.  workspace: at least q4_attention_decode_workspace_bytes,
+ * 256-byte aligned, zero-filled before its first use; its first 64 KiB are
+ * arrival counters that every call leaves at zero, the rest is scratch, so it
+ * can be shared with the library's other calls that take a workspace of this
+ * kind.  It does not depend on B or the lengths.  Calls that use one workspace
+ * must not overlap in time.  Results do not depend on timing, but for one
+ * sequence they may differ in their last bits with the others of its batch
+ * (the work is split by the lengths of all).
+ */
+size_t q4_attention_decode_workspace_bytes(int T, int Hq, int Hk, int D);
+int q4_attention_decode(const uint16_t* q, int B, int T, int Hq, int Hk, int D, int64_t q_stride, const q4_kv_cache* cache,
+                        const int32_t* table, int width, const int32_t* lengths, const int32_t* n_new, float scale, int window,
+                        uint16_t* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention over packed prompts: as above, with sequence b's queries in
+ * rows starts[b] .. starts[b + 1] of q [T, Hq, D] and its keys and values in
+ * rows key_starts[b] .. key_starts[b + 1] of k and v [S, Hk, D] (key_starts
+ * NULL: starts, and S = T).  Its last query sees its last key, each query
+ * before it one key less (so more keys than queries are a prefix that all
+ * see, and with fewer keys than queries the first ones see nothing), and of
+ * those the last `window` (0: all).  y [T, Hq, D]: rows that see nothing are 0;
+ * rows of no sequence are left as they are.  starts, key_starts int32 [B + 1],
+ * not decreasing; entries are taken within 0 .. T and 0 .. S.
+ *
+ * 1 <= T, S <= 2^22, 1 <= B <= 4096; the rest as above.  y must not overlap an
+ * input.
+ */
+int q4_attention_prefill(const uint16_t* q, int T, const uint16_t* k, const uint16_t* v, int S, int Hq, int Hk, int D, int64_t q_stride,
+                         int64_t k_stride, int64_t v_stride, const int32_t* starts, const int32_t* key_starts, int B, float scale,
+                         int window, uint16_t* y, void* stream);
+
+/*
  * Diagnostic dequantization of a whole matrix to fp32 w [N, K] (16-byte
  * aligned).  Bitwise equal to the format definitions above: int4 rounds
  * code*scale+min once; NVFP4 rounds e2m1*e4m3*G once (the first product is

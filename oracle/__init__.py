@@ -53,3 +53,9 @@ from .step import (  # noqa: F401
     verify_topk,
     verify_full,
 )
+from .attention import (  # noqa: F401
+    rope_heads,
+    e4m3_heads,
+    attend,
+    paged,
+)
