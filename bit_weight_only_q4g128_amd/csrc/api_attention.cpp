@@ -18,7 +18,7 @@ constexpr int kMaxTokens = 1 << 22;
 constexpr int kMaxHeads = 256;
 constexpr int kMaxNew = 64;                // new tokens of a sequence
 constexpr long kMaxKeys = 1l << 24;        // of a sequence's table
-constexpr int64_t kMaxStride = 1l << 32;
+constexpr int64_t kMaxStride = 1l << 24;
 
 bool heads_ok(int Hq, int Hk, int D) {
     return Hk >= 1 && Hq >= Hk && Hq <= kMaxHeads && Hq % Hk == 0 && (D == 64 || D == 128);

@@ -59,41 +59,58 @@ constexpr int kKBytes = (D / 8) * kColumn<D>;
 template <int D>
 constexpr int kStage = kKBytes<D> + kKeys * D * 2;         // bytes of a stage
 
-// A workgroup's share of 64 keys on the way to LDS.
+// A workgroup's share of 64 keys on the way to LDS.  A piece's place is a
+// uniform part (step, row of the piece) and one 32-bit offset of the thread.
 template <int D, int NW>
 struct Fetch {
     static constexpr int kThreads = 64 * NW;
     static constexpr int kK = kKeys * (D / 8) / kThreads;                // 16-byte pieces of K per thread
+    static constexpr int kKRows = kThreads / (D / 8);                    // keys between them
     static constexpr int kUnits = (kKeys / 4) * (D / 4);                 // units of V: 4 keys by 4 columns
     static constexpr int kV = (kUnits + kThreads - 1) / kThreads;
+    static constexpr int kVRows = 8 * kThreads / (D / 2);                // keys between them
     u32x4 k[kK];
     u32x2 v[kV][4];
 
+    // the thread's first piece of K, and first key of its first unit of V
+    static __device__ __forceinline__ int k_row(int tid) { return tid / (D / 8); }
+    static __device__ __forceinline__ int v_row(int tid) {
+        const int hs = tid / (D / 2);
+        return 16 * (hs >> 1) + 8 * (tid & 1) + 4 * (hs & 1);
+    }
+    static __device__ __forceinline__ int v_column(int tid) { return 4 * ((tid >> 1) & (D / 4 - 1)); }
+    static __device__ __forceinline__ bool has_v(int tid) { return kUnits >= kThreads || tid < kUnits; }
+
     __device__ __forceinline__ void load(const PrefillArgs& a, const uint16_t* kb, const uint16_t* vb, int key0, int lo, int hi, int tid) {
+        const uint8_t* k0 = reinterpret_cast<const uint8_t*>(kb + key0 * a.ks);
+        const uint8_t* v0 = reinterpret_cast<const uint8_t*>(vb + key0 * a.vs);
+        if (key0 >= lo && key0 + kKeys <= hi) {
+            const uint32_t k_at = (uint32_t)(k_row(tid) * (int)a.ks + 8 * (tid & (D / 8 - 1))) * 2u;
+            const uint32_t v_at = has_v(tid) ? (uint32_t)(v_row(tid) * (int)a.vs + v_column(tid)) * 2u : 0u;
+#pragma unroll
+            for (int i = 0; i < kK; ++i) k[i] = *reinterpret_cast<const u32x4*>(k0 + 2 * i * kKRows * a.ks + k_at);
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[i][r] = *reinterpret_cast<const u32x2*>(v0 + 2 * (i * kVRows + r) * a.vs + v_at);
+            return;
+        }
+        // the first or last keys: none is read behind them, and values that no
+        // row sees may be anything, and 0 * infinity is no 0
 #pragma unroll
         for (int i = 0; i < kK; ++i) {
-            const int at = i * kThreads + tid, key = min(key0 + at / (D / 8), hi - 1);
-            k[i] = *reinterpret_cast<const u32x4*>(kb + key * a.ks + 8 * (at & (D / 8 - 1)));
+            const int row = min(k_row(tid) + i * kKRows, hi - 1 - key0);
+            k[i] = *reinterpret_cast<const u32x4*>(k0 + ((long)row * a.ks + 8 * (tid & (D / 8 - 1))) * 2);
         }
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int at = i * kThreads + tid;
-            const int u = (at >> 1) & (D / 4 - 1), hs = at / (D / 2);
-            const int key = key0 + 16 * (hs >> 1) + 8 * (at & 1) + 4 * (hs & 1);
-            if (kUnits % kThreads && at >= kUnits) {
+        for (int i = 0; i < kV; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[i][r] = u32x2{0, 0};
-                break;
+            for (int r = 0; r < 4; ++r) {
+                const int row = v_row(tid) + i * kVRows + r;
+                const bool in = key0 + row >= lo && key0 + row < hi && has_v(tid);
+                v[i][r] = *reinterpret_cast<const u32x2*>(v0 + (in ? ((long)row * a.vs + v_column(tid)) * 2 : (lo - key0) * a.vs * 2));
+                if (!in) v[i][r] = u32x2{0, 0};
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[i][r] = *reinterpret_cast<const u32x2*>(vb + min(key + r, hi - 1) * a.vs + 4 * u);
-            // values that no row sees may be anything, and 0 * infinity is no 0
-            if (key0 < lo || key0 + kKeys > hi) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (key + r < lo || key + r >= hi) v[i][r] = u32x2{0, 0};
-            }
-        }
     }
     // takes infinities and NaNs out of V: whether there were any
     __device__ __forceinline__ bool tame() {
@@ -111,28 +128,23 @@ struct Fetch {
         return odd;
     }
     __device__ __forceinline__ void store(uint8_t* stage, int tid) const {
+        uint8_t* kt = stage + (tid & (D / 8 - 1)) * kColumn<D> + k_row(tid) * 16;
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            const int at = i * kThreads + tid;
-            *reinterpret_cast<u32x4*>(stage + (at & (D / 8 - 1)) * kColumn<D> + (at / (D / 8)) * 16) = k[i];
-        }
-        uint8_t* vt = stage + kKBytes<D>;
+        for (int i = 0; i < kK; ++i) *reinterpret_cast<u32x4*>(kt + i * kKRows * 16) = k[i];
+        if (!has_v(tid)) return;
+        const int u = (tid >> 1) & (D / 4 - 1), hs = tid / (D / 2);
+        // tile d % (D / 32), row d / (D / 32) of it for column d = 4 u + e
+        constexpr int kTiles = D / 32;
+        uint8_t* vt = stage + kKBytes<D> + ((hs >> 1) * kTiles * 2 + (hs & 1)) * 512 + (kTiles == 4 ? u : 2 * u) * 16 + (tid & 1) * 8;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int at = i * kThreads + tid;
-            const int u = (at >> 1) & (D / 4 - 1), hs = at / (D / 2);
-            if (kUnits % kThreads && at >= kUnits) break;
             const u32x2 t[4] = {u32x2{halves_lo(v[i][1].x, v[i][0].x), halves_lo(v[i][3].x, v[i][2].x)},
                                 u32x2{halves_hi(v[i][1].x, v[i][0].x), halves_hi(v[i][3].x, v[i][2].x)},
                                 u32x2{halves_lo(v[i][1].y, v[i][0].y), halves_lo(v[i][3].y, v[i][2].y)},
                                 u32x2{halves_hi(v[i][1].y, v[i][0].y), halves_hi(v[i][3].y, v[i][2].y)}};
-            // tile d % (D / 32), row d / (D / 32) of it for column d = 4 u + e
-            constexpr int kTiles = D / 32;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int tile = e & (kTiles - 1), m = kTiles == 4 ? u : 2 * u + (e >> 1);
-                *reinterpret_cast<u32x2*>(vt + (((hs >> 1) * kTiles + tile) * 2 + (hs & 1)) * 512 + m * 16 + (at & 1) * 8) = t[e];
-            }
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<u32x2*>(vt + i * (kVRows / 16) * kTiles * 1024 + (e & (kTiles - 1)) * 1024 + (kTiles == 4 ? 0 : (e >> 1) * 16)) = t[e];
         }
     }
 };
@@ -206,15 +218,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
         const int key0 = begin + i * kKeys;
         f32x16 z[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int j = 0; j < 16; ++j) z[0][j] = z[1][j] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) z[t][j] = 0.f;
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
+            for (int t = 0; t < 2; ++t) {
                 const bf16x8 k = *reinterpret_cast<const bf16x8*>(kt + (2 * j + half) * kColumn<D> + (32 * t + (lane & 31)) * 16);
                 z[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[j], z[t], 0, 0, 0);
             }
-        }
         const bool edge = partly(key0);
         if (edge) {
 #pragma unroll
@@ -229,7 +240,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
 #pragma unroll
         for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j >> 4][j & 15]);
         top = max_xor32(top);
-        if (__any(top > m)) {
+        // Weights may exceed 1: only a maximum that grew by more than 2^8
+        // rescales what is there, which after the first steps is rare.
+        if (__any((top - m) * p.c > 8.f)) {
             const float now = fmaxf(m, top);
             const float x = now == m ? 1.0f : __builtin_amdgcn_exp2f((m - now) * p.c);
             m = now;
@@ -239,13 +252,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
         }
         const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
         u32x4 pw[4];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][j & 15], p.c, -mc));
             const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][(j & 15) + 1], p.c, -mc));
-            l += x + y;
+            sum[(j >> 1) & 3] += x + y;
             pw[j >> 3][(j & 7) >> 1] = pack_bf16(x, y);
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll

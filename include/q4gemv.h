@@ -532,7 +532,8 @@ int q4_verify_full(const uint16_t* logits, int B, int D, int V, const int32_t* d
  * Heads have D = 64 or 128 values; Hq query heads share Hk key heads, query
  * head h with key head h / (Hq / Hk).  Arrays of heads are bf16
  * [tokens, heads, D] whose tokens lie `stride` elements apart (at least
- * heads * D, a multiple of 8), so that they may be parts of one product's rows.
+ * heads * D and at most 2^24, a multiple of 8), so that they may be parts of one
+ * product's rows.
  *
  * The cache is paged: pages of page_size tokens (16, 32, 64, 128 or 256), each
  * head's part of a page in one piece.  bf16, or, where scales are given,
