@@ -57,53 +57,65 @@ __device__ __forceinline__ float sum_xor16(float v) {
     return p.a + p.b;
 }
 
-// Where a running position falls among B sequences of count(b) units each:
-// the sequence, the units before the position inside it, and the units of all
-// sequences (seq is -1 where the position lies behind the last).  Every wave
-// works it out for itself: each lane counts a run of ceil(B / 64) <= 64
-// sequences, the wave sums the runs up to each lane, and the run that holds
-// the position is then spread over the lanes the same way.
-struct Place {
-    int seq;
-    int at;
-    long total;
+// ---------------------------------------------------------------------------
+// Where a workgroup's part of the work lies among B <= 4096 sequences of some
+// units each, which only the device knows.  Every wave works it out for itself:
+// a lane counts a run of ceil(B / 64) <= 64 sequences, the wave sums the runs up
+// to each lane, and the run that holds a position is then spread over the
+// lanes the same way.
+// ---------------------------------------------------------------------------
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+    return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
+}
+// Inclusive prefix sum over the 64 lanes (shifts within rows of 16, then the
+// row totals broadcast forward).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v = dpp_add<0x111>(v);
+    v = dpp_add<0x112>(v);
+    v = dpp_add<0x114>(v);
+    v = dpp_add<0x118>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    return dpp_add<0x143, 0xC>(v);
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+
+struct Runs {
+    int run;            // sequences of a lane
+    uint32_t upto;      // units up to this lane's run and with it
+    uint32_t total;     // of all
 };
-__device__ __forceinline__ long wave_scan(long v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int lo = __shfl_up((int)(uint32_t)v, d), hi = __shfl_up((int)(v >> 32), d);
-        if (lane >= d) v += ((long)hi << 32) | (uint32_t)lo;
-    }
-    return v;
-}
-__device__ __forceinline__ long wave_pick(long v, int lane) {
-    return ((long)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-}
 template <typename Count>
-__device__ __forceinline__ long count_all(int B, int lane, Count count, long& upto, int& run) {
-    run = (B + 63) >> 6;
-    long mine = 0;
-    for (int i = 0; i < run; ++i) {
-        const int b = lane * run + i;
+__device__ __forceinline__ Runs count_runs(int B, int lane, Count count) {
+    Runs r{(B + 63) >> 6, 0, 0};
+    uint32_t mine = 0;
+    for (int i = 0; i < r.run; ++i) {
+        const int b = lane * r.run + i;
         if (b < B) mine += count(b);
     }
-    upto = wave_scan(mine, lane);
-    return wave_pick(upto, 63);
+    r.upto = wave_scan(mine);
+    r.total = of_lane(r.upto, 63);
+    return r;
 }
+
+struct Place {
+    int seq;         // the sequence that holds a position
+    uint32_t at;     // units before the position inside it
+};
+// pos < r.total
 template <typename Count>
-__device__ __forceinline__ Place find_place(int B, int lane, long total, long upto, int run, long pos, Count count) {
-    if (pos < 0 || pos >= total) return Place{-1, 0, total};
-    int owner = __builtin_ctzll(__ballot(upto > pos));
-    long before = owner ? wave_pick(upto, owner - 1) : 0;
-    int b0 = owner * run;
-    if (run > 1) {
+__device__ __forceinline__ Place find_place(const Runs& r, int B, int lane, uint32_t pos, Count count) {
+    const int owner = __builtin_ctzll(__ballot(r.upto > pos));
+    uint32_t before = owner ? of_lane(r.upto, owner - 1) : 0;
+    int b0 = owner * r.run;
+    if (r.run > 1) {
         const int b = b0 + lane;
-        const long up = wave_scan(lane < run && b < B ? count(b) : 0, lane);
+        const uint32_t up = wave_scan(lane < r.run && b < B ? count(b) : 0);
         const int o = __builtin_ctzll(__ballot(up > pos - before));
-        if (o) before += wave_pick(up, o - 1);
+        if (o) before += of_lane(up, o - 1);
         b0 += o;
     }
-    return Place{b0, (int)(pos - before), total};
+    return Place{b0, pos - before};
 }
 
 }  // namespace q4

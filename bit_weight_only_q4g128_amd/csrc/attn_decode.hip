@@ -307,19 +307,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
     const int g = lane >> 4, c = lane & 15;
     const int B = p.a.B, HZ = p.a.Hk * p.Z;
 
-    auto count = [&](int b) -> long { return (long)span_of(p, b).blocks * HZ; };
-    long upto;
-    int run;
-    const long total = count_all(B, lane, count, upto, run);
+    auto count = [&](int b) -> uint32_t { return (uint32_t)span_of(p, b).blocks; };
+    const Runs runs = count_runs(B, lane, count);
+    const long total = (long)runs.total * HZ;
     const long W = total < p.W ? total : p.W;      // workgroups that have work
     const long w = blockIdx.x;
     if (w >= W) return;
     long pos = w * total / W;
     const long stop = (w + 1) * total / W;
-    const Place place = find_place(B, lane, total, upto, run, pos, count);
+    // a sequence's HZ units follow each other
+    const Place place = find_place(runs, B, lane, (uint32_t)(pos / HZ), count);
     int b = place.seq;
     Span sp = span_of(p, b);
-    int hz = place.at / sp.blocks, blk = place.at - hz * sp.blocks;
+    const uint32_t inside = place.at * HZ + (uint32_t)(pos % HZ);      // blocks before pos in its sequence
+    int hz = (int)(inside / sp.blocks), blk = (int)(inside % sp.blocks);
     const __amdgpu_buffer_rsrc_t parts = make_rsrc(p.part, 2u * kMaxWgs * kRows * kStride * 4u);
 
     while (pos < stop) {

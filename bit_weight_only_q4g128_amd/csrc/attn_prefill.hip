@@ -16,15 +16,20 @@
 // product's operand as they are, so P stays in registers, the maximum needs one
 // lane move and the sum none until the end.
 //
-// K and V pass through LDS once per workgroup, in the order in which the
-// operands read them (16 bytes a lane, consecutive): K in columns of 8 elements
-// (a column of 64 keys and 16 bytes more, so that a row's store touches every
-// bank once); V transposed, in units of 4 keys by 4 columns that a thread turns
-// in registers.  Two stages: the next 64 keys are stored while these are used,
-// and the ones after them are in flight in registers.
+// K and V go straight to LDS, once per workgroup and as they lie (16 bytes a
+// lane, no registers), some steps ahead of their use.  A row's 16-byte chunks
+// are exchanged on the way (the swizzle is on the memory side), so that the
+// operands' reads touch every bank once: K by rows, V by the transposing reads
+// that give a lane 4 keys of one column.
+//
+// Each wave computes a step's weights beside the matrix instructions of both
+// products: those of this step's values, and the next step's scores.
 #include "attention.h"
 #include "attn_common.h"
 #include "internal.h"
+#include "lds_load.h"
+
+#include <utility>
 
 namespace q4 {
 
@@ -32,6 +37,7 @@ namespace {
 
 constexpr int kKeys = 64;        // of a step
 constexpr int kWaveRows = 32;
+constexpr int kWaves = 4;            // waves; two workgroups share a CU
 
 struct PrefillParams {
     PrefillArgs a;
@@ -52,107 +58,60 @@ __device__ __forceinline__ Prompt prompt_of(const PrefillArgs& a, int b) {
     return s;
 }
 
+// Where things lie in LDS and which of them a lane takes.  A stage holds 64
+// rows of K, then of V, 2 D bytes each; 16-byte chunk c of row r of K sits at
+// chunk c ^ (r % 16) (D = 64: c ^ (r / 2 % 8)), so that a chunk of 16 rows
+// covers the banks once; of V at c ^ (r % 4 * 4) (D = 64: c ^ (r / 2 % 2 * 4)),
+// so that 64 bytes of 4 rows do.
 template <int D>
-constexpr int kColumn = kKeys * 16 + 16;                   // bytes of 8 elements' column of K
-template <int D>
-constexpr int kKBytes = (D / 8) * kColumn<D>;
-template <int D>
-constexpr int kStage = kKBytes<D> + kKeys * D * 2;         // bytes of a stage
+struct Tile {
+    static constexpr int kRow = 2 * D, kBytes = kKeys * kRow, kStage = 2 * kBytes;
+    static constexpr int kLoads = kBytes / 1024 / kWaves;            // 1 KB loads of a wave for 64 rows of K, or of V
+    static constexpr int kLoadRows = 1024 / kRow;
 
-// A workgroup's share of 64 keys on the way to LDS.  A piece's place is a
-// uniform part (step, row of the piece) and one 32-bit offset of the thread.
-template <int D, int NW>
-struct Fetch {
-    static constexpr int kThreads = 64 * NW;
-    static constexpr int kK = kKeys * (D / 8) / kThreads;                // 16-byte pieces of K per thread
-    static constexpr int kKRows = kThreads / (D / 8);                    // keys between them
-    static constexpr int kUnits = (kKeys / 4) * (D / 4);                 // units of V: 4 keys by 4 columns
-    static constexpr int kV = (kUnits + kThreads - 1) / kThreads;
-    static constexpr int kVRows = 8 * kThreads / (D / 2);                // keys between them
-    u32x4 k[kK];
-    u32x2 v[kV][4];
-
-    // the thread's first piece of K, and first key of its first unit of V
-    static __device__ __forceinline__ int k_row(int tid) { return tid / (D / 8); }
-    static __device__ __forceinline__ int v_row(int tid) {
-        const int hs = tid / (D / 2);
-        return 16 * (hs >> 1) + 8 * (tid & 1) + 4 * (hs & 1);
+    // (the chunk in LDS's place `lane` of the wave's loads, which are kWaves loads apart)
+    static __device__ __forceinline__ uint32_t k_chunk(int lane, int wave) {
+        return D == 128 ? (uint32_t)((lane & 15) ^ ((wave & 3) * 4 + (lane >> 4))) : (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4)));
     }
-    static __device__ __forceinline__ int v_column(int tid) { return 4 * ((tid >> 1) & (D / 4 - 1)); }
-    static __device__ __forceinline__ bool has_v(int tid) { return kUnits >= kThreads || tid < kUnits; }
-
-    __device__ __forceinline__ void load(const PrefillArgs& a, const uint16_t* kb, const uint16_t* vb, int key0, int lo, int hi, int tid) {
-        const uint8_t* k0 = reinterpret_cast<const uint8_t*>(kb + key0 * a.ks);
-        const uint8_t* v0 = reinterpret_cast<const uint8_t*>(vb + key0 * a.vs);
-        if (key0 >= lo && key0 + kKeys <= hi) {
-            const uint32_t k_at = (uint32_t)(k_row(tid) * (int)a.ks + 8 * (tid & (D / 8 - 1))) * 2u;
-            const uint32_t v_at = has_v(tid) ? (uint32_t)(v_row(tid) * (int)a.vs + v_column(tid)) * 2u : 0u;
-#pragma unroll
-            for (int i = 0; i < kK; ++i) k[i] = *reinterpret_cast<const u32x4*>(k0 + 2 * i * kKRows * a.ks + k_at);
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[i][r] = *reinterpret_cast<const u32x2*>(v0 + 2 * (i * kVRows + r) * a.vs + v_at);
-            return;
-        }
-        // the first or last keys: none is read behind them, and values that no
-        // row sees may be anything, and 0 * infinity is no 0
-#pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            const int row = min(k_row(tid) + i * kKRows, hi - 1 - key0);
-            k[i] = *reinterpret_cast<const u32x4*>(k0 + ((long)row * a.ks + 8 * (tid & (D / 8 - 1))) * 2);
-        }
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = v_row(tid) + i * kVRows + r;
-                const bool in = key0 + row >= lo && key0 + row < hi && has_v(tid);
-                v[i][r] = *reinterpret_cast<const u32x2*>(v0 + (in ? ((long)row * a.vs + v_column(tid)) * 2 : (lo - key0) * a.vs * 2));
-                if (!in) v[i][r] = u32x2{0, 0};
-            }
+    static __device__ __forceinline__ uint32_t v_chunk(int lane) {
+        return D == 128 ? (uint32_t)((lane & 15) ^ ((lane >> 4) * 4)) : (uint32_t)((lane & 7) ^ ((lane >> 4 & 1) * 4));
     }
-    // takes infinities and NaNs out of V: whether there were any
-    __device__ __forceinline__ bool tame() {
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t bits = odd_halves(v[i][r][x]);
-                    odd |= bits != 0;
-                    v[i][r][x] &= ~bits;
-                }
-        return odd;
+    // the lane's address in K's rows of a tile of 32 keys, chunk `half`; chunk 2 j + half is at ^ 32 j
+    static __device__ __forceinline__ uint32_t k_read(int lane) {
+        const int row = lane & 31, half = lane >> 5;
+        return (uint32_t)(row * kRow + ((half ^ (D == 128 ? row & 15 : row >> 1 & 7)) << 4));
     }
-    __device__ __forceinline__ void store(uint8_t* stage, int tid) const {
-        uint8_t* kt = stage + (tid & (D / 8 - 1)) * kColumn<D> + k_row(tid) * 16;
-#pragma unroll
-        for (int i = 0; i < kK; ++i) *reinterpret_cast<u32x4*>(kt + i * kKRows * 16) = k[i];
-        if (!has_v(tid)) return;
-        const int u = (tid >> 1) & (D / 4 - 1), hs = tid / (D / 2);
-        // tile d % (D / 32), row d / (D / 32) of it for column d = 4 u + e
-        constexpr int kTiles = D / 32;
-        uint8_t* vt = stage + kKBytes<D> + ((hs >> 1) * kTiles * 2 + (hs & 1)) * 512 + (kTiles == 4 ? u : 2 * u) * 16 + (tid & 1) * 8;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const u32x2 t[4] = {u32x2{halves_lo(v[i][1].x, v[i][0].x), halves_lo(v[i][3].x, v[i][2].x)},
-                                u32x2{halves_hi(v[i][1].x, v[i][0].x), halves_hi(v[i][3].x, v[i][2].x)},
-                                u32x2{halves_lo(v[i][1].y, v[i][0].y), halves_lo(v[i][3].y, v[i][2].y)},
-                                u32x2{halves_hi(v[i][1].y, v[i][0].y), halves_hi(v[i][3].y, v[i][2].y)}};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<u32x2*>(vt + i * (kVRows / 16) * kTiles * 1024 + (e & (kTiles - 1)) * 1024 + (kTiles == 4 ? 0 : (e >> 1) * 16)) = t[e];
-        }
+    // the lane's address in V's rows for columns 0 .. 31 of keys 4 half ..; columns 32 t are at ^ 64 t
+    static __device__ __forceinline__ uint32_t v_read(int lane) {
+        const int row = 4 * (lane >> 5) + (lane >> 2 & 3), turn = D == 128 ? row & 3 : row >> 1 & 1;
+        return (uint32_t)(row * kRow + (turn << 6) + (((lane >> 4 & 1) * 2 + (lane >> 1 & 1)) << 4) + (lane & 1) * 8);
     }
 };
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillParams p) {
-    constexpr int kRows = kWaveRows * NW, kTiles = D / 32;
-    __shared__ __align__(16) uint8_t lds[2 * kStage<D>];
+// f(0) .. f(N - 1), each with its number as a constant
+template <typename F, int... I>
+__device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// V^T's operand of 16 keys and 32 columns: this lane's column of keys 4 half ..
+// and 8 + 4 half .., at the rows' first address
+template <int D>
+__device__ __forceinline__ u32x4 columns(uint32_t at) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 8 * 2 * D));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(const PrefillParams p) {
+    using L = Tile<D>;
+    constexpr int kRows = kWaveRows * kWaves, kTiles = D / 32;
+    __shared__ __align__(2 * L::kStage) uint8_t lds[2 * L::kStage];
     __shared__ int s_odd;
     const PrefillArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -161,14 +120,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
     // The workgroup's rows.  Workgroups go to the XCDs in turn, so that with
     // the key head fastest a key head stays in one XCD's L2 (Hk dividing 8); a
     // prompt's last rows, which see most, come first.
-    auto count = [&](int b) -> long { return ((long)prompt_of(a, b).tokens * G + kRows - 1) / kRows; };
     const int head = blockIdx.x % a.Hk;
-    long upto;
-    int run;
-    const long total = count_all(a.B, lane, count, upto, run);
-    const Place place = find_place(a.B, lane, total, upto, run, total - 1 - blockIdx.x / a.Hk, count);
-    if (place.seq < 0) return;
-    const Prompt s = prompt_of(a, place.seq);
+    const uint32_t nth = blockIdx.x / a.Hk;
+    auto tiles_of = [&](const Prompt& s) { return ((uint32_t)s.tokens * (uint32_t)G + kRows - 1) / kRows; };
+    Prompt s{0, 0, 0, 0};
+    Place place;
+    if (a.B <= 64) {       // a prompt to a lane, read once
+        if (lane < a.B) s = prompt_of(a, lane);
+        const uint32_t upto = wave_scan(tiles_of(s)), total = of_lane(upto, 63);
+        if (nth >= total) return;
+        const uint32_t pos = total - 1 - nth;
+        const int owner = __builtin_ctzll(__ballot(upto > pos));
+        place = Place{owner, pos - (owner ? of_lane(upto, owner - 1) : 0u)};
+        s = Prompt{__builtin_amdgcn_readlane(s.q0, owner), __builtin_amdgcn_readlane(s.tokens, owner), __builtin_amdgcn_readlane(s.k0, owner),
+                   __builtin_amdgcn_readlane(s.keys, owner)};
+    } else {
+        auto count = [&](int b) -> uint32_t { return tiles_of(prompt_of(a, b)); };
+        const Runs runs = count_runs(a.B, lane, count);
+        if (nth >= runs.total) return;
+        place = find_place(runs, a.B, lane, runs.total - 1 - nth, count);
+        s = prompt_of(a, place.seq);
+    }
     const int row0 = place.at * kRows, rows = min(kRows, s.tokens * G - row0);
     const int more = s.keys - s.tokens;                   // keys before the first token's own
     const int first = row0 / G, last = (row0 + rows - 1) / G;
@@ -192,95 +164,228 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
-    float m = -__builtin_inff(), l = 0.f;
+    float m = -__builtin_inff(), sum[4] = {0.f, 0.f, 0.f, 0.f};
 
     const uint16_t* kb = a.k + (long)s.k0 * a.ks + head * D;
     const uint16_t* vb = a.v + (long)s.k0 * a.vs + head * D;
-    Fetch<D, NW> f;
-    auto partly = [&](int key0) { return key0 + kKeys > first_end || (a.window && key0 < last_end - a.window); };
-    auto put = [&](int i) {       // the fetched keys into their stage
-        if (partly(begin + i * kKeys) && f.tame()) s_odd = 1;
-        f.store(lds + (i & 1) * kStage<D>, tid);
-    };
-    if (tid == 0) s_odd = 0;
-    __syncthreads();
-    if (steps > 0) {
-        f.load(a, kb, vb, begin, lo, hi, tid);
-        put(0);
-        if (steps > 1) f.load(a, kb, vb, begin + kKeys, lo, hi, tid);
-    }
-    for (int i = 0; i < steps; ++i) {
-        __syncthreads();
-        if (i + 1 < steps) put(i + 1);
-        if (i + 2 < steps) f.load(a, kb, vb, begin + (i + 2) * kKeys, lo, hi, tid);
-        const uint8_t* kt = lds + (i & 1) * kStage<D>;
-        const uint8_t* vt = kt + kKBytes<D>;
+    auto partly = [&](int i) {       // some rows see keys of step i that others do not
         const int key0 = begin + i * kKeys;
-        f32x16 z[2];
+        return key0 + kKeys > first_end || (a.window && key0 < last_end - a.window);
+    };
+
+    const uint32_t base = lds_address(lds);
+    const uint32_t k_off = (uint32_t)((wave * L::kLoadRows + lane / (D / 8)) * (int)a.ks) * 2u + L::k_chunk(lane, wave) * 16u;
+    const uint32_t v_off = (uint32_t)((wave * L::kLoadRows + lane / (D / 8)) * (int)a.vs) * 2u + L::v_chunk(lane) * 16u;
+    // Step i's keys (or values) on their way to an LDS stage; behind the last
+    // key, and from the last step on, zeros.  A call takes the next step, into
+    // the other stage than the one before it.
+    struct Stream {
+        const uint8_t* from;
+        uint32_t row, to;      // bytes of a row
+        int left;              // keys
+    };
+    auto fetch = [&](Stream& f, uint32_t off) {
+        const int n = f.left;
+        const i32x4 r = rsrc_words(f.from, n >= kKeys ? (kKeys - 1) * f.row + 2 * D : n > 0 ? (uint32_t)(n - 1) * f.row + 2 * D : 0u);
+#pragma unroll
+        for (int j = 0; j < L::kLoads; ++j)
+            to_lds16(r, off, (uint32_t)(j * kWaves * L::kLoadRows) * f.row, f.to + (uint32_t)((j * kWaves + wave) * 1024));
+        if (n > 0) f.from += (uint64_t)kKeys * f.row;
+        f.left = n - kKeys;
+        f.to ^= L::kStage;
+    };
+    // (stages lie kStage apart, a power of two at a multiple of twice its size)
+    Stream ks{reinterpret_cast<const uint8_t*>(kb + begin * a.ks), (uint32_t)a.ks * 2u, base, hi - begin};
+    Stream vs{reinterpret_cast<const uint8_t*>(vb + begin * a.vs), (uint32_t)a.vs * 2u, base + L::kBytes, hi - begin};
+    auto fetch_k = [&] { fetch(ks, k_off); };
+    auto fetch_v = [&] { fetch(vs, v_off); };
+    // Values that no row sees may be anything, and 0 * infinity is no 0: where
+    // rows see different keys, step i's values, there already, become 0 outside
+    // [lo, hi), and infinities and NaNs are put off (s_odd).
+    auto tame = [&](int i) {
+        uint8_t* v = lds + (i & 1) * L::kStage + L::kBytes;
+        bool odd = false;
+        for (int at = tid; at < kKeys * D / 8; at += 64 * kWaves) {
+            const int key = begin + i * kKeys + at / (D / 8);
+            u32x4 w = *reinterpret_cast<const u32x4*>(v + at * 16);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t bits = odd_halves(w[x]);
+                const bool in = key >= lo && key < hi;
+                odd |= in && bits;
+                w[x] = in ? w[x] & ~bits : 0u;
+            }
+            *reinterpret_cast<u32x4*>(v + at * 16) = w;
+        }
+        if (odd) s_odd = 1;
+    };
+
+    const uint32_t k_read = L::k_read(lane), v_read = L::v_read(lane);
+    auto scores = [&](f32x16 (&z)[2], int i) {
+        const uint32_t at = base + (uint32_t)(i & 1) * L::kStage + k_read;
 #pragma unroll
         for (int j = 0; j < 16; ++j) z[0][j] = z[1][j] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const bf16x8 k = *reinterpret_cast<const bf16x8*>(kt + (2 * j + half) * kColumn<D> + (32 * t + (lane & 31)) * 16);
+                const bf16x8 k = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)((at ^ (32 * j)) + 32 * t * L::kRow);
                 z[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[j], z[t], 0, 0, 0);
             }
-        const bool edge = partly(key0);
-        if (edge) {
+    };
+    auto largest = [&](const f32x16 (&z)[2]) {
+        float top = z[0][0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j >> 4][j & 15]);
+        return top;
+    };
+    // the scores' weights into the sums and outputs, with the values of step i
+    auto outputs = [&](const f32x16 (&z)[2], int i) {
+        const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
+        const uint32_t at = base + (uint32_t)(i & 1) * L::kStage + L::kBytes + v_read;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = 8 * (k & 1) + 2 * j;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 1][e], p.c, -mc));
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 1][e + 1], p.c, -mc));
+                w[j] = pack_bf16(x, y);
+                sum[j] = dot2(w[j], 0x3F803F80u, sum[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, columns<D>((at ^ (64 * t)) + 16 * k * L::kRow)),
+                                                               __builtin_bit_cast(bf16x8, w), o[t], 0, 0, 0);
+        }
+    };
+    // step i's scores: what rows do not see taken out, and the maximum
+    auto settle = [&](f32x16 (&z)[2], float top, int i) {
+        if (partly(i)) {
+            const int here = begin + i * kKeys + 4 * half, from = low - here, to = end - here;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int key = key0 + 32 * t + 8 * (j >> 2) + 4 * half + (j & 3);
-                    z[t][j] = key >= low && key < end ? z[t][j] : -__builtin_inff();
+                    const int key = 32 * t + 8 * (j >> 2) + (j & 3);
+                    z[t][j] = key >= from && key < to ? z[t][j] : -__builtin_inff();
                 }
+            top = max_xor32(largest(z));
         }
-        float top = z[0][0];
-#pragma unroll
-        for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j >> 4][j & 15]);
-        top = max_xor32(top);
         // Weights may exceed 1: only a maximum that grew by more than 2^8
         // rescales what is there, which after the first steps is rare.
         if (__any((top - m) * p.c > 8.f)) {
             const float now = fmaxf(m, top);
             const float x = now == m ? 1.0f : __builtin_amdgcn_exp2f((m - now) * p.c);
             m = now;
-            l *= x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] *= x;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) o[t] *= x;
         }
+    };
+    // One step: this step's weights and outputs beside the next one's scores,
+    // in this order, which nothing changes: a matrix instruction, the fragment of
+    // the fourth one after it, and a share of the arithmetic, which takes as
+    // long as the matrix instruction.  A pair of weights begins (its scores
+    // become exponentials) in one slot and ends (rounded, summed) in the next;
+    // the next scores' maximum follows when they are there.
+    auto step = [&](f32x16 (&z)[2], f32x16 (&next)[2], int i) {
+        constexpr int kN = D / 8, kAhead = 4, kSpread = 2 * kN * 13 / 16;      // products of either kind; slots in which pairs begin
+        fetch_k();       // of step i + 2
+        fetch_v();       // of step i + 1
+        const uint32_t k_at = base + (uint32_t)((i + 1) & 1) * L::kStage + k_read;
+        const uint32_t v_at = base + (uint32_t)(i & 1) * L::kStage + L::kBytes + v_read;
         const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
-        u32x4 pw[4];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        u32x4 f[2 * kN], w[4];
+        float e[16][2], top[2] = {-__builtin_inff(), -__builtin_inff()};
+        auto read = [&](auto at) {
+            constexpr int j = decltype(at)::value;
+            if constexpr (j < kN) f[j] = *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)((k_at ^ (32 * (j >> 1))) + 32 * (j & 1) * L::kRow);
+            else if constexpr (j < 2 * kN) f[j] = columns<D>((v_at ^ (64 * ((j - kN) % kTiles))) + 16 * ((j - kN) / kTiles) * L::kRow);
+        };
+        each(read, std::make_integer_sequence<int, kAhead>());
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][j & 15], p.c, -mc));
-            const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][(j & 15) + 1], p.c, -mc));
-            sum[(j >> 1) & 3] += x + y;
-            pw[j >> 3][(j & 7) >> 1] = pack_bf16(x, y);
+        for (int j = 0; j < 16; ++j) next[0][j] = next[1][j] = 0.f;
+        __builtin_amdgcn_sched_barrier(0);
+        each([&](auto slot) {
+            constexpr int j = decltype(slot)::value;
+            const bf16x8 x = __builtin_bit_cast(bf16x8, f[j]);
+            if constexpr (j < kN) next[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[j >> 1], next[j & 1], 0, 0, 0);
+            else o[(j - kN) % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, w[(j - kN) / kTiles]), o[(j - kN) % kTiles], 0, 0, 0);
+            read(std::integral_constant<int, j + kAhead>{});
+            each([&](auto pair) {
+                constexpr int n = decltype(pair)::value;
+                if constexpr (n * kSpread / 16 + 1 == j) {
+                    w[n >> 2][n & 3] = pack_bf16(e[n][0], e[n][1]);
+                    sum[n & 3] = dot2(w[n >> 2][n & 3], 0x3F803F80u, sum[n & 3]);
+                    asm volatile("" : "+v"(sum[n & 3]));
+                }
+                if constexpr (n * kSpread / 16 == j) {
+                    float a = z[n >> 3][2 * (n & 7)], b = z[n >> 3][2 * (n & 7) + 1];
+                    asm volatile("" : "+v"(a), "+v"(b));
+                    e[n][0] = __builtin_amdgcn_exp2f(__builtin_fmaf(a, p.c, -mc));
+                    e[n][1] = __builtin_amdgcn_exp2f(__builtin_fmaf(b, p.c, -mc));
+                    asm volatile("" : "+v"(e[n][0]), "+v"(e[n][1]));
+                }
+                if constexpr (kN + 2 + n * (kN - 2) / 16 == j) {
+                    top[n & 1] = fmaxf(fmaxf(top[n & 1], next[n & 1][n & 14]), next[n & 1][(n & 14) + 1]);
+                    asm volatile("" : "+v"(top[n & 1]));
+                }
+            }, std::make_integer_sequence<int, 16>());
+            __builtin_amdgcn_sched_barrier(0);
+        }, std::make_integer_sequence<int, 2 * kN>());
+        settle(next, max_xor32(fmaxf(top[0], top[1])), i + 1);
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): this step's loads are there
+        phase();
+        if (partly(i + 1)) {
+            tame(i + 1);
+            __syncthreads();
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const bf16x8 v = *reinterpret_cast<const bf16x8*>(vt + ((k * kTiles + t) * 2 + half) * 512 + (lane & 31) * 16);
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, __builtin_bit_cast(bf16x8, pw[k]), o[t], 0, 0, 0);
-            }
+    };
+    if (tid == 0) s_odd = 0;
+    if (steps > 0) {
+        fetch_k();
+        fetch_v();
+        fetch_k();
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        if (partly(0)) tame(0);
+        f32x16 z0[2], z1[2];
+        scores(z0, 0);
+        settle(z0, max_xor32(largest(z0)), 0);
+        __syncthreads();       // K's first stage is free
+        int i = 0;
+        for (; i + 2 < steps; i += 2) {
+            step(z0, z1, i);
+            step(z1, z0, i + 1);
+        }
+        if (i + 1 < steps) {
+            step(z0, z1, i);
+            outputs(z1, i + 1);
+        } else {
+            outputs(z0, i);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);      // nothing is on its way to LDS
     }
+    float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     __syncthreads();
     if (s_odd) {
         // Rare: where some rows see keys that others do not, some values are
         // infinities or NaNs.  Those values alone, which were left out above,
         // key by key into the rows that see them.
+        const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
 #pragma unroll 1
-        for (int key0 = begin; key0 < hi; key0 += kKeys) {
-            if (!partly(key0)) continue;
-            f.load(a, kb, vb, key0, lo, hi, tid);
-            f.store(lds, tid);
+        for (int i = 0; i < steps; ++i) {
+            if (!partly(i)) continue;
+            const int key0 = begin + i * kKeys;
+            Stream k1{reinterpret_cast<const uint8_t*>(kb + key0 * a.ks), (uint32_t)a.ks * 2u, base, hi - key0};
+            Stream v1{reinterpret_cast<const uint8_t*>(vb + key0 * a.vs), (uint32_t)a.vs * 2u, base + L::kBytes, hi - key0};
+            fetch(k1, k_off);
+            fetch(v1, v_off);
+            __builtin_amdgcn_s_waitcnt(0x0F70);
             __syncthreads();
-            const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 f32x16 z;
@@ -288,7 +393,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
                 for (int j = 0; j < 16; ++j) z[j] = 0.f;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    const bf16x8 x = *reinterpret_cast<const bf16x8*>(lds + (2 * j + half) * kColumn<D> + (32 * (k >> 1) + (lane & 31)) * 16);
+                    const bf16x8 x = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)(((base + k_read) ^ (32 * j)) + 32 * (k >> 1) * L::kRow);
                     z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[j], z, 0, 0, 0);
                 }
                 float w[8];
@@ -298,12 +403,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
 #pragma unroll 1
                 for (int j = 0; j < 16; ++j) {
                     const uint32_t keep = (j >> 3) == half ? ((j & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-                    const int at = (j & 7) >> 1, key = key0 + 16 * k + 8 * ((j >> 2) & 1) + 4 * (j >> 3) + (j & 3);
+                    const int at = (j & 7) >> 1, key = begin + i * kKeys + 16 * k + 8 * ((j >> 2) & 1) + 4 * (j >> 3) + (j & 3);
                     const u32x4 mask{at == 0 ? keep : 0u, at == 1 ? keep : 0u, at == 2 ? keep : 0u, at == 3 ? keep : 0u};
                     const bool in = key >= low && key < end;
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
-                        u32x4 v = *reinterpret_cast<const u32x4*>(lds + kKBytes<D> + ((k * kTiles + t) * 2 + half) * 512 + (lane & 31) * 16);
+                        u32x4 v = columns<D>(((base + L::kBytes + v_read) ^ (64 * t)) + 16 * k * L::kRow);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) v[x] &= odd_halves(v[x]) & mask[x];
                         f32x16 none;
@@ -324,35 +429,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prefill_kernel(const PrefillP
     const float f0 = 1.0f / l;
     uint16_t* y = a.out + ((long)(s.q0 + token) * a.Hq + q_head) * D;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        // columns (D / 32) (8 x + 4 half + b) + tile, b = 0 .. 3
-        constexpr int kRun = D / 8;
-        uint32_t w[kRun / 2];
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int t = 0; t < kTiles; t += 2)
-                w[(b * kTiles + t) >> 1] = none ? 0u : pack_bf16(o[t][4 * x + b] * f0, o[t + 1][4 * x + b] * f0);
-#pragma unroll
-        for (int i = 0; i < kRun / 8; ++i)
-            *reinterpret_cast<u32x4*>(y + 2 * kRun * x + kRun * half + 8 * i) = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
-    }
+        for (int x = 0; x < 4; ++x)      // columns 32 t + 8 x + 4 half ..
+            *reinterpret_cast<u32x2*>(y + 32 * t + 8 * x + 4 * half) =
+                u32x2{none ? 0u : pack_bf16(o[t][4 * x] * f0, o[t][4 * x + 1] * f0), none ? 0u : pack_bf16(o[t][4 * x + 2] * f0, o[t][4 * x + 3] * f0)};
 }
 
-template <int D, int NW>
+template <int D>
 hipError_t launch(const PrefillParams& p, hipStream_t s) {
-    const long rows = kWaveRows * NW;
+    const long rows = kWaveRows * kWaves;
     const long tiles = ((long)p.a.T * p.G + rows - 1) / rows + p.a.B;     // at least the sum of the prompts' own
-    return launch_kernel(attn_prefill_kernel<D, NW>, dim3((unsigned)(tiles * p.a.Hk)), dim3(64 * NW), 0, s, p);
+    return launch_kernel(attn_prefill_kernel<D>, dim3((unsigned)(tiles * p.a.Hk)), dim3(64 * kWaves), 0, s, p);
 }
 
 }  // namespace
 
 hipError_t launch_attention_prefill(const PrefillArgs& a, hipStream_t s) {
     const PrefillParams p{a, a.scale * kLog2e, a.Hq / a.Hk};
-    const bool wide = (long)a.T * a.Hq >= 256l * 256;
-    if (a.D == 128) return wide ? launch<128, 8>(p, s) : launch<128, 4>(p, s);
-    return wide ? launch<64, 8>(p, s) : launch<64, 4>(p, s);
+    return a.D == 128 ? launch<128>(p, s) : launch<64>(p, s);
 }
 
 }  // namespace q4

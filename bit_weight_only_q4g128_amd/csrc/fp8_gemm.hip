@@ -20,6 +20,7 @@
 
 #include "fp8.h"
 #include "internal.h"
+#include "lds_load.h"
 #include "topk.h"
 
 namespace q4 {
@@ -27,7 +28,6 @@ namespace q4 {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 // the weights' scales, through the scalar cache (a vector load would join the
 // queue of the loads to LDS, and its wait would wait for all of them)
 typedef const __attribute__((address_space(4))) float const_float;
@@ -35,26 +35,6 @@ typedef const __attribute__((address_space(4))) float const_float;
 __device__ __forceinline__ u32x4 ld16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
-// Loads straight to LDS, 16 or 4 bytes per lane in lane order from LDS address
-// `to` on.  Assembly, because around the builtin the compiler waits for every
-// such load before any read of LDS, also of another stage; the kernels below
-// wait by themselves (vmcnt, then a barrier).  Nothing is written to registers;
-// the compiler puts `to` into m0 (a wait state before its use).  There is no
-// memory clobber, which would bring those waits back: that LDS is not read before
-// the load has ended, nor written while it is read, rests on the s_waitcnt and
-// phase() (a barrier across which nothing moves) around it.
-// The descriptor's check covers the sum of a lane's and the scalar offset and
-// does not wrap (measured with both past it): what lies behind gives zeros.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes) {
-    const uint64_t b = reinterpret_cast<uintptr_t>(base);
-    return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), (int)bytes, kBufferFlags};
-}
-__device__ __forceinline__ void to_lds16(i32x4 r, uint32_t off, uint32_t soff, uint32_t to) {
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(r), "s"(soff), "{m0}"(to));
-}
-__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
-
 __device__ __forceinline__ f32x4 mfma(const u32x4 (&a)[2], const u32x4 (&b)[2]) {
     const i32x8 av = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
     const i32x8 bv = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
@@ -303,13 +283,6 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Group p) {
 // c ^ (r % 8) takes 8.  The swizzle is on the memory side of the load: LDS is
 // written in lane order.
 // ---------------------------------------------------------------------------
-// Ends a phase of the tile kernel: nothing moves across, no wait is implied.
-__device__ __forceinline__ void phase() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 template <int BM, int BN>
 struct TileLds {
     static constexpr int kXStage = BM * 128, kWStage = BN * 128;
