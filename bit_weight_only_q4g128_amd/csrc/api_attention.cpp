@@ -18,6 +18,8 @@ constexpr int kMaxTokens = 1 << 22;
 constexpr int kMaxHeads = 256;
 constexpr int kMaxNew = 64;                // new tokens of a sequence
 constexpr long kMaxKeys = 1l << 24;        // of a sequence's table
+constexpr long kMaxUnits = 1l << 31;       // of a decode call
+constexpr size_t kMaxRows = 1ul << 31;     // of a cache, each head's counted
 constexpr int64_t kMaxStride = 1l << 24;
 
 bool heads_ok(int Hq, int Hk, int D) {
@@ -48,7 +50,9 @@ int check_cache(const q4_kv_cache* c, int Hk, int D, q4::Cache* out, CacheRanges
     if (!c->k || !c->v || !c->k_scale != !c->v_scale) return Q4_EINVAL_PTR;
     if (c->pages < 1 || c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return Q4_EINVAL_SHAPE;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return Q4_EALIGN;
-    const size_t rows = (size_t)c->pages * Hk * c->page_size, bytes = rows * D * (c->k_scale ? 1 : 2);
+    const size_t rows = (size_t)c->pages * Hk * c->page_size;
+    if (rows >= kMaxRows) return Q4_EINVAL_SHAPE;
+    const size_t bytes = rows * D * (c->k_scale ? 1 : 2);
     *ranges = CacheRanges{{range_of(c->k, bytes), range_of(c->v, bytes), c->k_scale ? range_of(c->k_scale, rows * 4) : Range{0, 0},
                            c->v_scale ? range_of(c->v_scale, rows * 4) : Range{0, 0}}};
     *out = q4::Cache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale, c->pages,
@@ -123,6 +127,9 @@ int q4_attention_decode(const uint16_t* q, int B, int T, int Hq, int Hk, int D, 
     const int rc = check_cache(cache, Hk, D, &c, &cr);
     if (rc) return rc;
     if ((long)width << c.shift > kMaxKeys) return Q4_EINVAL_SHAPE;
+    // a window of all keys is none
+    const q4::DecodeArgs a{q, y, table, lengths, n_new, (long)q_stride, B, T, Hq, Hk, D, width, window >= kMaxKeys ? 0 : window, scale};
+    if (q4::attention_decode_units(a, c) >= kMaxUnits) return Q4_EINVAL_SHAPE;
     if (!aligned(q, 16) || !aligned(table, 4) || !aligned(lengths, 4) || !aligned(n_new, 4) || !aligned(y, 16) || !aligned(workspace, 256))
         return Q4_EALIGN;
     const size_t need = q4::attention_decode_ws_bytes(T, Hq, Hk, D);
@@ -134,8 +141,6 @@ int q4_attention_decode(const uint16_t* q, int B, int T, int Hq, int Hk, int D, 
     for (const Range& r : in)
         if (overlaps(out, r) || overlaps(ws, r)) return Q4_EALIAS;
     if (overlaps(out, ws)) return Q4_EALIAS;
-    // a window of all keys is none
-    const q4::DecodeArgs a{q, y, table, lengths, n_new, (long)q_stride, B, T, Hq, Hk, D, width, window >= kMaxKeys ? 0 : window, scale};
     const hipError_t e = q4::launch_attention_decode(a, c, workspace, reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? Q4_OK : Q4_ELAUNCH;
 }

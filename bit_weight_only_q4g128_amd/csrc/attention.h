@@ -45,6 +45,8 @@ struct DecodeArgs {
     float scale;
 };
 // ws: a workspace whose first 64 KiB are arrival counters (zero, left zero).
+// Tiles of work at the most: (sequence, key head, rows, 32 keys); they have to be below 2^31.
+long attention_decode_units(const DecodeArgs& a, const Cache& cache);
 size_t attention_decode_ws_bytes(int T, int Hq, int Hk, int D);
 hipError_t launch_attention_decode(const DecodeArgs& a, const Cache& cache, void* ws, hipStream_t s);
 

@@ -536,7 +536,7 @@ int q4_verify_full(const uint16_t* logits, int B, int D, int V, const int32_t* d
  * product's rows.
  *
  * The cache is paged: pages of page_size tokens (16, 32, 64, 128 or 256), each
- * head's part of a page in one piece.  bf16, or, where scales are given,
+ * head's part of a page in one piece; pages * Hk * page_size < 2^31.  bf16, or, where scales are given,
  * float8_e4m3fn codes with one fp32 scale per token and head
  * (value = code * scale).
  */
@@ -596,8 +596,9 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * rounded to bf16 before it multiplies its value.
  *
  * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
- * 2^24; scale finite and > 0; window >= 0.  Alignment: q and y 16 bytes, table,
- * lengths, n_new 4.  workspace: at least q4_attention_decode_workspace_bytes,
+ * 2^24, and B * Hk * (ceil(width * page_size / 32) + 8), times ceil(T * Hq / Hk / 32)
+ * where T * Hq / Hk is above 16, below 2^31; scale finite and > 0; window >= 0.
+ * Alignment: q and y 16 bytes, table, lengths, n_new 4.  workspace: at least q4_attention_decode_workspace_bytes,
  * 256-byte aligned, zero-filled before its first use; its first 64 KiB are
  * arrival counters that every call leaves at zero, the rest is scratch, so it
  * can be shared with the library's other calls that take a workspace of this

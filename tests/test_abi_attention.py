@@ -29,7 +29,7 @@ def rope(q=at(0), k=at(1), v=at(2), T=4, Hq=16, Hk=4, D=128, qs=2048, ks=512, vs
 
 CACHE = [
     (dict(pages=0), ESHAPE), (dict(page_size=8), ESHAPE), (dict(page_size=24), ESHAPE), (dict(page_size=512), ESHAPE),
-    (dict(page_size=0), ESHAPE), (dict(page_size=-16), ESHAPE), (dict(pages=-1), ESHAPE),
+    (dict(page_size=0), ESHAPE), (dict(page_size=-16), ESHAPE), (dict(pages=-1), ESHAPE), (dict(pages=1 << 25), ESHAPE),
 ]
 
 
@@ -81,7 +81,7 @@ def decode(q=at(0), B=3, T=2, Hq=16, Hk=4, D=128, qs=2048, table=at(1), width=8,
     (dict(k=None), EPTR), (dict(v=None), EPTR), (dict(ks=at(22)), EPTR),
     (dict(B=0), ESHAPE), (dict(B=4097), ESHAPE), (dict(T=0), ESHAPE), (dict(T=65), ESHAPE), (dict(Hq=15, qs=1920), ESHAPE), (dict(Hk=0), ESHAPE),
     (dict(Hk=32), ESHAPE), (dict(Hq=512, qs=1 << 16), ESHAPE), (dict(D=32), ESHAPE), (dict(qs=2044), ESHAPE), (dict(qs=2040), ESHAPE),
-    (dict(width=0), ESHAPE), (dict(width=(1 << 20) + 1), ESHAPE), (dict(window=-1), ESHAPE), (dict(scale=0.0), ESHAPE),
+    (dict(width=0), ESHAPE), (dict(width=(1 << 20) + 1), ESHAPE), (dict(B=4096, width=1 << 20), ESHAPE), (dict(B=4096, T=64, width=1 << 17), ESHAPE), (dict(window=-1), ESHAPE), (dict(scale=0.0), ESHAPE),
     (dict(scale=-1.0), ESHAPE), (dict(scale=math.inf), ESHAPE), (dict(scale=math.nan), ESHAPE),
     (dict(q=at(0) + 8), EALIGN), (dict(table=at(1) + 2), EALIGN), (dict(lengths=at(2) + 1), EALIGN), (dict(n_new=at(3) + 2), EALIGN),
     (dict(y=at(4) + 8), EALIGN), (dict(ws=at(5) + 128), EALIGN), (dict(nb=65536), ESCRATCH), (dict(nb=0), ESCRATCH),

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import synth
-from attention_util import check_decode, values
+from attention_util import attention_bound, check_decode, values, within
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +106,16 @@ def test_split_and_joined(q4, ws, lengths, P, e4m3):
     """One long sequence over all workgroups, ragged ones, more sequences than
     workgroups, a long one among short ones."""
     check(q4, ws, problem(lengths, 1, 4, 2, 128, P, 4, e4m3))
+
+
+@pytest.mark.parametrize("T,Hq,Hk", [(1, 2, 2), (1, 12, 1), (8, 2, 1), (8, 6, 2), (40, 1, 1)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_parts(q4, ws, T, Hq, Hk, e4m3):
+    """Long sequences after each other, each over many workgroups, the first and
+    the last of them shared: parts joined in groups.  Twice in one workspace."""
+    p = problem([9000, 14000, 33, 16000, 4500], T, Hq, Hk, 64, 64, 11, e4m3)
+    y = check(q4, ws, p)
+    assert torch.equal(check(q4, ws, p).view(torch.int16), y.view(torch.int16))
 
 
 @pytest.mark.parametrize("B", [64, 65, 129, 4096])
@@ -309,6 +320,27 @@ def test_long_cache_offsets(q4, ws):
     far = torch.where(table >= 0, table + (pages - n), -1)
     y = q4.attention_decode(q.cuda(), cache, far.cuda(), lens.cuda(), workspace=ws)
     assert torch.equal(y, run(q4, ws, q, small, table, lens))
+
+
+@pytest.mark.parametrize("D,T", [(64, 1), (128, 8)])
+def test_table_in_parts(q4, ws, D, T):
+    """So many keys that a workgroup takes its pages in parts: a table that goes
+    over a few pages again and again, 2^24 keys less the new ones' last page.  All
+    keys weigh alike in every round, so the result is attention over one round (a
+    whole number of rounds for the last row's; the rows before it miss keys among
+    2^24).  A lane adds 2^24 * Hk / 512 / 16 weights at most, and 512 parts meet."""
+    Hk, P, n = 4, 16, 64
+    rounds = (1 << 20) // n
+    q, cache, _, _ = problem([n * P], T, 8, Hk, D, P, 21, spare=0)
+    table = torch.arange(n, dtype=torch.int32).repeat(rounds)[None]
+    lens = torch.tensor([1 << 24], dtype=torch.int32)
+    y = values(run(q4, ws, q, cache, table, lens))[0]
+    k, v = (values(t).transpose(1, 0, 2, 3).reshape(Hk, n * P, D) for t in cache)
+    for h in range(Hk):
+        rows = values(q)[0, :, 2 * h:2 * h + 2].reshape(2 * T, D)
+        want, mass, score = oracle.attend(rows, k[h], v[h], [n * P] * (2 * T), D ** -0.5)
+        bound = attention_bound(want, mass, score, (1 << 24) * Hk // 512 // 16 + 512, D) + T * 2.0 ** -14
+        within(y[:, 2 * h:2 * h + 2].reshape(2 * T, D), want, bound, f"head {h}")
 
 
 def test_binding_refusals(q4, ws):
