@@ -39,13 +39,14 @@
 //
 // Measured (16 heads over 4, D = 128; us, and the bytes of q, y and the keys
 // and values seen at that rate):
-//   one sequence, 2304 keys, bf16                    9.2
-//   48 sequences up to 2304 keys, bf16                28   4.2 TB/s
-//   48 sequences up to 4099, 5 rows each, e4m3        38   2.9 TB/s
-//   one sequence, 131071 keys, bf16                   52   5.2 TB/s
-//   32 sequences of 32768 keys, bf16                 324   6.6 TB/s
-// where a copy of 2 GiB moves 4.9 TB/s, both directions counted.  The last is
-// the memory's rate; before it stand the launch, the lengths, pages and heads
+//   one sequence, 2304 keys, bf16                    9.3
+//   48 sequences up to 2304 keys, bf16                26   4.5 TB/s
+//   48 sequences up to 4099, 5 rows each, e4m3        37   3.0 TB/s
+//   one sequence, 131071 keys, bf16                   49   5.5 TB/s
+//   32 sequences of 32768 keys, bf16                 325   6.6 TB/s
+// the same cache again and again; another one every time (1.2 GB of them in
+// turn): 10.1, 29, 40, 64 and 347.  A copy of 2 GiB moves 4.9 TB/s, both
+// directions counted.  The last is the memory's rate; before it stand the launch, the lengths, pages and heads
 // one after the other, and the join, some 6 us together.
 #include "attention.h"
 #include "attn_common.h"
@@ -127,13 +128,16 @@ struct Keys {
     u32x4 k[2][kLoads];
     float scale;          // of key 8 g + c % 8
 
+    // (V's loads take whole rows and are marked as read once, K's take 64 bytes of
+    // a row and are not: both marked cost 4 to 15 % where the cache is in reach of
+    // the last level, 2 % where it is not; neither marked costs 4 to 12 % there)
     __device__ __forceinline__ void load(const DecodeParams& p, const Rows& at, int lane) {
         const uint8_t* from = p.cache.k + (uint64_t)at.k * kRow + 16 * (lane >> 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int s = 0; s < kLoads; ++s)
-                k[t][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + 4 * t * kRow + 64 * s));
+                k[t][s] = *reinterpret_cast<const u32x4*>(from + 4 * t * kRow + 64 * s);
         if constexpr (kE4m3) scale = p.cache.ks[(uint64_t)at.v + (lane & 7)];
     }
 };
