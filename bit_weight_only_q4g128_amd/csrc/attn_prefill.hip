@@ -24,6 +24,18 @@
 //
 // Each wave computes a step's weights beside the matrix instructions of both
 // products: those of this step's values, and the next step's scores.
+//
+// Measured (16 heads; us, and the products of the keys that rows see):
+//   one prompt of 77 tokens, D = 128 over 4                    7.0
+//   48 prompts up to 2304 tokens, D = 128 over 4               457    809 TFLOP/s
+//   5 prompts up to 1999 tokens behind 2048 keys, window
+//   1024, D = 64 over 8                                         42    560 TFLOP/s
+//   one prompt of 16384 tokens, D = 128 over 4                1021   1077 TFLOP/s
+// where the library's product of 8192 x 8192 x 8192 reaches 1605.  The long
+// prompt runs at 1.9 GHz, the board's power being what bounds it then; half the
+// heads' columns leave the exponentials half as much to hide behind; short
+// prompts pay for masked halves of the diagonal's steps and some 6000 cycles a
+// workgroup before its first product.
 #include "attention.h"
 #include "attn_common.h"
 #include "internal.h"
@@ -37,7 +49,13 @@ namespace {
 
 constexpr int kKeys = 64;        // of a step
 constexpr int kWaveRows = 32;
-constexpr int kWaves = 4;            // waves; two workgroups share a CU
+// Waves of a workgroup: 8 took 520 us for the packed prompts below where 4 took
+// 507 (and 64 for the window where 4 took 49), 2 took 652.
+constexpr int kWaves = 4;
+// Workgroups that share a CU.  Registers set them; with heads of 64 columns a
+// third one pays though five registers are then spilled (window: 50 -> 43 us,
+// long prompts of such heads 182 -> 171).
+constexpr int workgroups(int D) { return D == 64 ? 3 : 2; }
 
 struct PrefillParams {
     PrefillArgs a;
@@ -108,7 +126,7 @@ __device__ __forceinline__ u32x4 columns(uint32_t at) {
 }
 
 template <int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(const PrefillParams p) {
+__global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kernel(const PrefillParams p) {
     using L = Tile<D>;
     constexpr int kRows = kWaveRows * kWaves, kTiles = D / 32;
     __shared__ __align__(2 * L::kStage) uint8_t lds[2 * L::kStage];
@@ -292,7 +310,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(const Pref
     // become exponentials) in one slot and ends (rounded, summed) in the next;
     // the next scores' maximum follows when they are there.
     auto step = [&](f32x16 (&z)[2], f32x16 (&next)[2], int i) {
-        constexpr int kN = D / 8, kAhead = 4, kSpread = 2 * kN * 13 / 16;      // products of either kind; slots in which pairs begin
+        constexpr int kN = D / 8, kSpread = 2 * kN * 13 / 16;      // products of either kind; slots in which pairs begin
+        constexpr int kAhead = D == 64 ? 2 : 4;      // fragments on their way (more registers with three workgroups a CU: 1 % slower)
         fetch_k();       // of step i + 2
         fetch_v();       // of step i + 1
         const uint32_t k_at = base + (uint32_t)((i + 1) & 1) * L::kStage + k_read;
@@ -424,16 +443,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(const Pref
         }
     }
     l = sum_xor32(l);
-    if (!row_in) return;
     const bool none = l == 0.f;
     const float f0 = 1.0f / l;
     uint16_t* y = a.out + ((long)(s.q0 + token) * a.Hq + q_head) * D;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)      // columns 32 t + 8 x + 4 half ..
-            *reinterpret_cast<u32x2*>(y + 32 * t + 8 * x + 4 * half) =
-                u32x2{none ? 0u : pack_bf16(o[t][4 * x] * f0, o[t][4 * x + 1] * f0), none ? 0u : pack_bf16(o[t][4 * x + 2] * f0, o[t][4 * x + 3] * f0)};
+        for (int x = 0; x < 4; x += 2) {
+            // columns 32 t + 8 x + 4 half .. and 8 more: of both halves' for one
+            // half, the 8 more for the other, 16 bytes a store
+            const auto lo = __builtin_amdgcn_permlane32_swap(pack_bf16(o[t][4 * x] * f0, o[t][4 * x + 1] * f0),
+                                                             pack_bf16(o[t][4 * x + 4] * f0, o[t][4 * x + 5] * f0), false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(pack_bf16(o[t][4 * x + 2] * f0, o[t][4 * x + 3] * f0),
+                                                             pack_bf16(o[t][4 * x + 6] * f0, o[t][4 * x + 7] * f0), false, false);
+            if (row_in) *reinterpret_cast<u32x4*>(y + 32 * t + 8 * (x + half)) = none ? u32x4{0, 0, 0, 0} : u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
 }
 
 template <int D>
