@@ -961,6 +961,12 @@ def rope_cache(q, k, v=None, positions=None, inv_freq=None, q_norm=None, k_norm=
     return q_out, k_out
 
 
+def _window(window):
+    if not -2 ** 31 <= window < 2 ** 31:
+        raise ValueError("window must be below 2^31")
+    return window
+
+
 def attention_decode_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
     """Bytes of workspace attention_decode uses for T new tokens a sequence."""
     return int(lib.q4_attention_decode_workspace_bytes(T, Hq, Hk, D))
@@ -1004,7 +1010,7 @@ def attention_decode(q, cache, table, lengths, n_new=None, scale=None, window: i
     else:
         _tensor(out, "out", _U16, (B, T, Hq, D), index)
     _enqueue(index, lib.q4_attention_decode, q.data_ptr(), B, T, Hq, Hk, D, stride, cp, tp, width, lp,
-             _optional(n_new, "n_new", _I32, (B,), index), D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+             _optional(n_new, "n_new", _I32, (B,), index), D ** -0.5 if scale is None else scale, _window(window), out.data_ptr(),
              *_scratch(workspace, index))
     return out
 
@@ -1034,5 +1040,5 @@ def attention_prefill(q, k, v, starts, key_starts=None, scale=None, window: int 
     else:
         _tensor(out, "out", _U16, (T, Hq, D), index)
     _enqueue(index, lib.q4_attention_prefill, q.data_ptr(), T, k.data_ptr(), v.data_ptr(), S, Hq, Hk, D, qs, ks, vs, sp, kp, n - 1,
-             D ** -0.5 if scale is None else scale, window, out.data_ptr())
+             D ** -0.5 if scale is None else scale, _window(window), out.data_ptr())
     return out

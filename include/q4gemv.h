@@ -536,9 +536,9 @@ int q4_verify_full(const uint16_t* logits, int B, int D, int V, const int32_t* d
  * product's rows.
  *
  * The cache is paged: pages of page_size tokens (16, 32, 64, 128 or 256), each
- * head's part of a page in one piece; pages * Hk * page_size < 2^31.  bf16, or, where scales are given,
- * float8_e4m3fn codes with one fp32 scale per token and head
- * (value = code * scale).
+ * head's part of a page in one piece; pages * Hk * page_size < 2^31.  bf16, or,
+ * where scales are given, float8_e4m3fn codes with one fp32 scale per token and
+ * head (value = code * scale).
  */
 typedef struct q4_kv_cache {
     void* k;              /* bf16 or e4m3 [pages, Hk, page_size, D], 16-byte aligned */
@@ -592,17 +592,18 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
  * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
  * Keys and values that a row does not see have no effect on it, whatever they
- * hold.  Softmax and sums are fp32; a weight (times an 8-bit value's scale) is
- * rounded to bf16 before it multiplies its value.
+ * hold.  Scores, softmax and sums are fp32 (a score that leaves its range is
+ * infinite); a weight (times an 8-bit value's scale) is rounded to bf16 before it
+ * multiplies its value.
  *
  * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
  * 2^24, and B * Hk * (ceil(width * page_size / 32) + 8), times ceil(T * Hq / Hk / 32)
  * where T * Hq / Hk is above 16, below 2^31; scale finite and > 0; window >= 0.
- * Alignment: q and y 16 bytes, table, lengths, n_new 4.  workspace: at least q4_attention_decode_workspace_bytes,
- * 256-byte aligned, zero-filled before its first use; its first 64 KiB are
- * arrival counters that every call leaves at zero, the rest is scratch, so it
- * can be shared with the library's other calls that take a workspace of this
- * kind.  It does not depend on B or the lengths.  Calls that use one workspace
+ * Alignment: q and y 16 bytes, table, lengths, n_new 4.
+ * workspace: at least q4_attention_decode_workspace_bytes, 256-byte aligned,
+ * zero-filled before its first use; its first 64 KiB are arrival counters that
+ * every call leaves at zero, the rest is scratch, so it can be shared with the
+ * library's other calls that take a workspace of this kind.  It does not depend on B or the lengths.  Calls that use one workspace
  * must not overlap in time.  Results do not depend on timing, but for one
  * sequence they may differ in their last bits with the others of its batch
  * (the work is split by the lengths of all).

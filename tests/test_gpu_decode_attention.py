@@ -118,6 +118,31 @@ def test_many_parts(q4, ws, T, Hq, Hk, e4m3):
     assert torch.equal(check(q4, ws, p).view(torch.int16), y.view(torch.int16))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,T,Hq,Hk", [(70, 40, 2, 1), (64, 9, 8, 2), (200, 2, 32, 2)])
+def test_many_rows_of_many_sequences(q4, ws, B, T, Hq, Hk, e4m3):
+    """A padded batch: sequences of no tokens and of fewer new ones than T."""
+    p = problem([(11 * b * b) % 170 if b % 9 else 0 for b in range(B)], T, Hq, Hk, 64, 16, 21, e4m3)
+    n = torch.tensor([(5 * b) % (T + 1) if b % 9 else 0 for b in range(B)], dtype=torch.int32)
+    check(q4, ws, p, n)
+    check(q4, ws, p, n, 37)
+
+
+@pytest.mark.parametrize("T", [1, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_do_not_meet(q4, ws, T, bad):
+    """A head of q that is no number is that head's row alone."""
+    q, cache, table, lens = problem([150, 33], T, 8, 2, 64, 16, 22)
+    clean = check(q4, ws, (q, cache, table, lens))
+    odd = q.clone()
+    odd[0, T - 1, 2], odd[1, 0, 5] = bad, bad
+    y = run(q4, ws, odd, cache, table, lens)
+    for at in ((0, T - 1, 2), (1, 0, 5)):
+        assert torch.isnan(y[at]).all()
+        y[at] = clean[at]
+    check_decode(y, q, cache, table, lens, None, 64 ** -0.5, 0)
+
+
 @pytest.mark.parametrize("B", [64, 65, 129, 4096])
 def test_many_sequences(q4, ws, B):
     """The search for a workgroup's place among sequences."""
@@ -351,7 +376,8 @@ def test_binding_refusals(q4, ws):
     call()
     for kw in (dict(q=q[0]), dict(q=q[:1]), dict(table=table[:1]), dict(lengths=lens[:1]), dict(cache=cache[:1]), dict(table=table[0]),
                dict(cache=tuple(t.transpose(1, 2) for t in cache)), dict(out=q[:, :1]), dict(n_new=lens[:1]), dict(q=q.transpose(2, 3)),
-               dict(table=table.cpu()), dict(q=q.transpose(0, 1)), dict(cache=(cache[0], cache[1][:-1]))):
+               dict(table=table.cpu()), dict(q=q.transpose(0, 1)), dict(cache=(cache[0], cache[1][:-1])), dict(window=2 ** 32 + 5),
+               dict(window=1 - 2 ** 32)):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(q=q.float()), dict(table=table.long()), dict(lengths=lens.long()), dict(cache=tuple(t.float() for t in cache)),

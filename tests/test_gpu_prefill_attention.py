@@ -117,6 +117,20 @@ def test_infinite_values_that_are_seen(q4):
         assert np.isfinite(np.delete(y[t], [3, 5, 9], axis=1)).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_do_not_meet(q4, bad):
+    """A head of q that is no number is that head's row alone."""
+    q, k, v, st, ks = problem([150, 33], [150, 33], 8, 2, 64, 12)
+    clean = check(q4, (q, k, v, st, ks))
+    odd = q.clone()
+    odd[70, 2], odd[160, 5] = bad, bad
+    y = run(q4, odd, k, v, st, ks)
+    for at in ((70, 2), (160, 5)):
+        assert torch.isnan(y[at]).all()
+        y[at] = clean[at]
+    check_prefill(y, q, k, v, st, ks, 64 ** -0.5, 0)
+
+
 def test_scores_of_any_size(q4):
     p = problem([150, 40], [150, 40], 4, 2, 128, 6)
     for scale in (1.0, 1e-3):
@@ -259,7 +273,8 @@ def test_binding_refusals(q4):
     call = lambda **kw: q4.attention_prefill(**{**dict(q=q, k=k, v=v, starts=st), **kw})  # noqa: E731
     call()
     for kw in (dict(k=k[:-1]), dict(v=v[:-1]), dict(k=k[:, :, :32]), dict(starts=st[None]), dict(key_starts=st[:1]), dict(out=q[:-1]),
-               dict(q=q[:, 0]), dict(q=q.transpose(0, 1)), dict(starts=st.cpu()), dict(k=k.cpu())):
+               dict(q=q[:, 0]), dict(q=q.transpose(0, 1)), dict(starts=st.cpu()), dict(k=k.cpu()), dict(window=2 ** 32 + 5),
+               dict(window=1 - 2 ** 32)):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(starts=st.long()), dict(q=q.half()), dict(v=v.float()), dict(q=3)):
