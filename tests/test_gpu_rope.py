@@ -78,7 +78,7 @@ def check_cache(cache, before, k_want, k_bound, v, slots):
 
 
 @pytest.mark.parametrize("T,Hq,Hk,D,P", [(1, 16, 4, 128, 16), (3, 14, 2, 64, 32), (5, 1, 1, 128, 16), (48, 16, 4, 128, 64), (1, 8, 8, 64, 256),
-                                         (1030, 5, 3, 64, 16), (1027, 12, 1, 128, 128)])
+                                         (1030, 5, 3, 64, 16), (1027, 12, 1, 128, 128), (2570, 5, 3, 64, 16), (2563, 12, 1, 128, 128)])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("strided", [False, True])
@@ -97,9 +97,10 @@ def test_norm_rotate_append(q4, T, Hq, Hk, D, P, inter, e4m3, strided):
 @pytest.mark.parametrize("D,rot", [(128, 0), (128, 16), (128, 64), (128, 112), (64, 32), (64, 48), (64, 0)])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("norms", [(0, 0), (1, 0), (0, 1)])
-def test_parts_of_it(q4, D, rot, inter, norms):
+@pytest.mark.parametrize("T", [37, 2569])
+def test_parts_of_it(q4, T, D, rot, inter, norms):
     """Partial rotations, none, either norm; without a cache; in place."""
-    T, Hq, Hk = 37, 6, 2
+    Hq, Hk = 6, 2
     q, k, v, pos, slots, qw, kw, cache = problem(T, Hq, Hk, D, 16, 1, strided=True)
     f = freqs(rot) if rot else None
     args = dict(positions=pos.cuda() if rot else None, inv_freq=f.cuda() if rot else None, q_norm=qw.cuda() if norms[0] else None,
