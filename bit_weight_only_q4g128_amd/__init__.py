@@ -1,7 +1,8 @@
 """Python binding of libq4gemv.so (4-bit weight-only dequant-GEMV for gfx950).
 
 Argument marshalling only: every step runs in the HIP library.  Tensors must
-be CUDA (ROCm) tensors, contiguous, with the dtypes the C header documents;
+be CUDA (ROCm) tensors, contiguous (tokens of heads may lie apart, where a
+function says so), with the dtypes the C header documents;
 calls are enqueued on torch's current stream of the tensors' device.  There is
 no CPU fallback: importing fails loudly if the library has not been built
 (``python bit_weight_only_q4g128_amd/_build.py``).
