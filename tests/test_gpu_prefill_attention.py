@@ -40,7 +40,8 @@ def check(q4, p, window=0, scale=None):
     return y
 
 
-HEADS = [(16, 4, 128), (4, 4, 64), (7, 1, 128), (8, 2, 64), (3, 3, 128), (24, 1, 64)]
+HEADS = [(16, 4, 128), (4, 4, 64), (7, 1, 128), (8, 2, 64), (3, 3, 128), (24, 1, 64),
+         (72, 72, 64), (144, 72, 128)]     # of so many heads: more workgroups than CUs
 
 
 @pytest.mark.parametrize("Hq,Hk,D", HEADS)
