@@ -202,15 +202,23 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
         uint32_t row, to;      // bytes of a row
         int left;              // keys
     };
-    auto fetch = [&](Stream& f, uint32_t off) {
+    auto source = [&](const Stream& f) {
         const int n = f.left;
-        const i32x4 r = rsrc_words(f.from, n >= kKeys ? (kKeys - 1) * f.row + 2 * D : n > 0 ? (uint32_t)(n - 1) * f.row + 2 * D : 0u);
-#pragma unroll
-        for (int j = 0; j < L::kLoads; ++j)
-            to_lds16(r, off, (uint32_t)(j * kWaves * L::kLoadRows) * f.row, f.to + (uint32_t)((j * kWaves + wave) * 1024));
-        if (n > 0) f.from += (uint64_t)kKeys * f.row;
-        f.left = n - kKeys;
+        return rsrc_words(f.from, n >= kKeys ? (kKeys - 1) * f.row + 2 * D : n > 0 ? (uint32_t)(n - 1) * f.row + 2 * D : 0u);
+    };
+    auto load = [&](const Stream& f, i32x4 r, uint32_t off, int j) {
+        to_lds16(r, off, (uint32_t)(j * kWaves * L::kLoadRows) * f.row, f.to + (uint32_t)((j * kWaves + wave) * 1024));
+    };
+    auto advance = [&](Stream& f) {
+        if (f.left > 0) f.from += (uint64_t)kKeys * f.row;
+        f.left -= kKeys;
         f.to ^= L::kStage;
+    };
+    auto fetch = [&](Stream& f, uint32_t off) {
+        const i32x4 r = source(f);
+#pragma unroll
+        for (int j = 0; j < L::kLoads; ++j) load(f, r, off, j);
+        advance(f);
     };
     // (stages lie kStage apart, a power of two at a multiple of twice its size)
     Stream ks{reinterpret_cast<const uint8_t*>(kb + begin * a.ks), (uint32_t)a.ks * 2u, base, hi - begin};
@@ -312,8 +320,6 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
     auto step = [&](f32x16 (&z)[2], f32x16 (&next)[2], int i) {
         constexpr int kN = D / 8, kSpread = 2 * kN * 13 / 16;      // products of either kind; slots in which pairs begin
         constexpr int kAhead = D == 64 ? 2 : 4;      // fragments on their way (more registers with three workgroups a CU: 1 % slower)
-        fetch_k();       // of step i + 2
-        fetch_v();       // of step i + 1
         const uint32_t k_at = base + (uint32_t)((i + 1) & 1) * L::kStage + k_read;
         const uint32_t v_at = base + (uint32_t)(i & 1) * L::kStage + L::kBytes + v_read;
         const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
@@ -325,6 +331,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
             else if constexpr (j < 2 * kN) f[j] = columns<D>((v_at ^ (64 * ((j - kN) % kTiles))) + 16 * ((j - kN) / kTiles) * L::kRow);
         };
         each(read, std::make_integer_sequence<int, kAhead>());
+        const i32x4 from_k = source(ks), from_v = source(vs);      // keys of step i + 2, values of step i + 1
 #pragma unroll
         for (int j = 0; j < 16; ++j) next[0][j] = next[1][j] = 0.f;
         __builtin_amdgcn_sched_barrier(0);
@@ -334,6 +341,10 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
             if constexpr (j < kN) next[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[j >> 1], next[j & 1], 0, 0, 0);
             else o[(j - kN) % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, w[(j - kN) / kTiles]), o[(j - kN) % kTiles], 0, 0, 0);
             read(std::integral_constant<int, j + kAhead>{});
+            if constexpr (j < 2 * L::kLoads) {      // (all of them ahead of the first: 1 to 6 % slower)
+                if constexpr (j < L::kLoads) load(ks, from_k, k_off, j);
+                else load(vs, from_v, v_off, j - L::kLoads);
+            }
             each([&](auto pair) {
                 constexpr int n = decltype(pair)::value;
                 if constexpr (n * kSpread / 16 + 1 == j) {
@@ -355,6 +366,8 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
             }, std::make_integer_sequence<int, 16>());
             __builtin_amdgcn_sched_barrier(0);
         }, std::make_integer_sequence<int, 2 * kN>());
+        advance(ks);
+        advance(vs);
         settle(next, max_xor32(fmaxf(top[0], top[1])), i + 1);
         __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0): this step's loads are there
         phase();
