@@ -27,10 +27,10 @@
 //
 // Measured (16 heads; us, and the products of the keys that rows see):
 //   one prompt of 77 tokens, D = 128 over 4                    7.0
-//   48 prompts up to 2304 tokens, D = 128 over 4               457    809 TFLOP/s
+//   48 prompts up to 2304 tokens, D = 128 over 4               457    808 TFLOP/s
 //   5 prompts up to 1999 tokens behind 2048 keys, window
-//   1024, D = 64 over 8                                         42    560 TFLOP/s
-//   one prompt of 16384 tokens, D = 128 over 4                1021   1077 TFLOP/s
+//   1024, D = 64 over 8                                         41    578 TFLOP/s
+//   one prompt of 16384 tokens, D = 128 over 4                1008   1091 TFLOP/s
 // where the library's product of 8192 x 8192 x 8192 reaches 1605.  The long
 // prompt runs at 1.9 GHz, the board's power being what bounds it then; half the
 // heads' columns leave the exponentials half as much to hide behind; short
