@@ -889,6 +889,6 @@ const char* q4gemv_strerror(int status) {
     }
 }
 
-int q4gemv_version(void) { return 120; }
+int q4gemv_version(void) { return 130; }
 
 }  // extern "C"

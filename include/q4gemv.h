@@ -527,7 +527,7 @@ int q4_verify_full(const uint16_t* logits, int B, int D, int V, const int32_t* d
  * A decoder layer's attention: what lies between its q, k, v projections and
  * its o projection.  The Rumik TTS Fast Inference post fuses "rotary position,
  * cache" operations ("What Made It Faster"), the rumik-oss-1-int4 card's engine
- * lists flash-decoding attention ("Running it").
+ * lists the decode steps' attention among its kernels ("Running it").
  *
  * Heads have D = 64 or 128 values; Hq query heads share Hk key heads, query
  * head h with key head h / (Hq / Hk).  Arrays of heads are bf16
