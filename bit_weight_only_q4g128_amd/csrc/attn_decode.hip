@@ -23,8 +23,8 @@
 //   V: lane (g, c) loads D / 16 columns of keys 8 g .. 8 g + 7, which after a
 //     transposition inside the lane (v_perm) is V^T's operand, the column
 //     e + (D / 16) c being row c of tile e.
-// A wave's next 32 keys are in flight while it works on the present ones, or
-// its next 64 where a row has less than 256 bytes (16 KB a wave, 128 KB a CU).
+// A wave's next 32 keys are in flight while it works on the present ones (16 KB
+// a wave, 128 KB a CU; 64 keys of smaller rows are no faster).
 // The pages of a workgroup's keys lie in LDS by then, a load apart from them
 // and not in front of every step's.
 //
@@ -318,7 +318,6 @@ __device__ __forceinline__ void add_key_by_key(State<D, NT>& st, int e, u32x4 v,
 
 template <int D, bool kE4m3, int NT>
 __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodeParams p) {
-    constexpr int kDepth = Keys<D, kE4m3>::kRow == 256 ? 1 : 2;     // steps of a wave in flight: 16 KB, 8 KB for the smallest rows
     constexpr int E = D / 16, kRows = 16 * NT, kStride = D + 4;     // a row of LDS and of a part: D outputs, then its maximum and sum
     __shared__ __align__(16) float s_o[kWaves * kRows * kStride];
     int32_t* s_table = reinterpret_cast<int32_t*>(s_o);      // the pages of the keys at hand, before the waves meet
@@ -391,8 +390,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
         const int seen_lo = p.a.window ? max(0, first_end - p.a.window) : 0, last_low = p.a.window ? sp.len - p.a.window : 0;
         const int hi = min(sp.hi, sp.lo + (tile + tiles) * kTile);
 
-        Keys<D, kE4m3> keys[kDepth];
-        Values<D, kE4m3> values[kDepth];
+        Keys<D, kE4m3> keys;
+        Values<D, kE4m3> values;
         int later = -1, later2 = -1;      // of a sequence's first or last keys
         const int shift = p.cache.shift, in_page = (1 << shift) - 1;
         const int32_t* table = p.a.table + (long)b * p.a.width;
@@ -414,73 +413,66 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
                             key_v < end && page_v >= 0};
             };
             int k0 = part + wave * kTile;
-            bool held[kDepth];
+            bool held = false;
+            if (k0 < end) {
+                const Rows at = rows_at(k0);
+                held = at.held;
+                keys.load(p, at, lane);
+                values.load(p, at, lane);
+            }
+            for (; k0 < end; k0 += kBlock) {
+                const bool here = held, more = k0 + kBlock < end;
+                const Rows at = rows_at(k0 + kBlock);
+                float z[NT][8];
+                scores<D, kE4m3, NT>(z, keys, q, p.c);
+                held = at.held;
+                if (more) keys.load(p, at, lane);
+                const bool edge = k0 + kTile > first_end || k0 < last_low || k0 < seen_lo || __any(!here);
+                if (edge) hide_scores<D, NT>(z, st, k0 + 8 * g, here);
+                weights<D, NT>(st, z);
+                bf16x8 pr[NT];
+                values.template operands<NT>(pr, z, edge);
+                // (new tokens are at most 64, so that at most one step of a wave lies
+                // where the keys that rows see begin, and one where they end)
+                const bool partly = sp.n > 1 && (k0 + kTile > first_end || k0 < last_low);
+                bool odd = false;
 #pragma unroll
-            for (int r = 0; r < kDepth; ++r)
-                if (k0 + r * kBlock < end) {
-                    const Rows at = rows_at(k0 + r * kBlock);
-                    held[r] = at.held;
-                    keys[r].load(p, at, lane);
-                    values[r].load(p, at, lane);
-                }
-            while (k0 < end) {
+                for (int x = 0; x < E / 2; ++x) {
+                    uint32_t v[8];
+                    values.pairs(v, x);
+                    if (edge) odd |= hide_values(v, k0 + 8 * g, seen_lo, sp.hi, here, partly);
 #pragma unroll
-                for (int r = 0; r < kDepth; ++r) {
-                    if (kDepth > 1 && k0 >= end) break;
-                    const bool here = held[r], more = k0 + kDepth * kBlock < end;
-                    const Rows at = rows_at(k0 + kDepth * kBlock);
-                    float z[NT][8];
-                    scores<D, kE4m3, NT>(z, keys[r], q, p.c);
-                    held[r] = at.held;
-                    if (more) keys[r].load(p, at, lane);
-                    const bool edge = k0 + kTile > first_end || k0 < last_low || k0 < seen_lo || __any(!here);
-                    if (edge) hide_scores<D, NT>(z, st, k0 + 8 * g, here);
-                    weights<D, NT>(st, z);
-                    bf16x8 pr[NT];
-                    values[r].template operands<NT>(pr, z, edge);
-                    // (new tokens are at most 64, so that at most one step of a wave lies
-                    // where the keys that rows see begin, and one where they end)
-                    const bool partly = sp.n > 1 && (k0 + kTile > first_end || k0 < last_low);
-                    bool odd = false;
+                    for (int h = 0; h < 2; ++h) {
+                        const bf16x8 vt = __builtin_bit_cast(bf16x8, values_of(v, h));
 #pragma unroll
-                    for (int x = 0; x < E / 2; ++x) {
-                        uint32_t v[8];
-                        values[r].pairs(v, x);
-                        if (edge) odd |= hide_values(v, k0 + 8 * g, seen_lo, sp.hi, here, partly);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const bf16x8 vt = __builtin_bit_cast(bf16x8, values_of(v, h));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) st.o[n][2 * x + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[n], st.o[n][2 * x + h], 0, 0, 0);
-                        }
+                        for (int n = 0; n < NT; ++n) st.o[n][2 * x + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[n], st.o[n][2 * x + h], 0, 0, 0);
                     }
-                    if (edge && __any(odd)) {
-                        later2 = later;
-                        later = k0;
-                    }
-                    if (more) values[r].load(p, at, lane);
-                    k0 += kBlock;
                 }
+                if (edge && __any(odd)) {
+                    later2 = later;
+                    later = k0;
+                }
+                if (more) values.load(p, at, lane);
             }
             // rare: the (at most two) steps whose infinities and NaNs were left out above
 #pragma unroll 1
             for (; later >= 0; later = later2, later2 = -1) {
                 const Rows at = rows_at(later);
-                keys[0].load(p, at, lane);
-                values[0].load(p, at, lane);
+                keys.load(p, at, lane);
+                values.load(p, at, lane);
                 float z[NT][8];
-                scores<D, kE4m3, NT>(z, keys[0], q, p.c);
+                scores<D, kE4m3, NT>(z, keys, q, p.c);
                 hide_scores<D, NT>(z, st, later + 8 * g, at.held);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) z[n][j] = __builtin_amdgcn_exp2f(z[n][j] - (st.m[n] == -__builtin_inff() ? 0.f : st.m[n]));
                 bf16x8 pr[NT];
-                values[0].template operands<NT>(pr, z, true);
+                values.template operands<NT>(pr, z, true);
 #pragma unroll
                 for (int x = 0; x < E / 2; ++x) {
                     uint32_t v[8];
-                    values[0].pairs(v, x);
+                    values.pairs(v, x);
                     hide_values(v, later + 8 * g, seen_lo, sp.hi, at.held, false);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) add_key_by_key<D, NT>(st, 2 * x + h, values_of(v, h), pr, later, g);
