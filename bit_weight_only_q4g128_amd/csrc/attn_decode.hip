@@ -62,11 +62,13 @@ constexpr int kTile = 32;                    // keys of a wave's step
 constexpr int kBlock = kTile * kWaves;       // keys of a workgroup's step
 constexpr int kMaxWgs = (int)(kWsCounterBytes / kCtrStride);      // 512: two a CU
 constexpr int kAhead = 4;                    // parts that a thread has in flight when it joins (8: up to 1 us more)
-// A unit of more parts than this (for every set of threads) is joined in two
-// turns.  One workgroup fetches parts at some 10 bytes a cycle: 128 parts of
-// 32 rows took 64 us more in one turn, of 4 rows 6; with 8 parts (or 16 of 8
-// rows, 32 of 4) and less the second arrival costs more, 1 us.
-constexpr int kManyParts = 8;
+// A unit of more parts than kManyParts (for every set of threads) is joined in
+// turns, by groups of up to kGroup (for every set), about as many as there are
+// in a group.  One workgroup fetches parts at some 10 bytes a cycle: 128 parts of
+// 32 rows took 128 us with the attention in one turn, 60 in groups of 16 and 8,
+// 57 in groups of 4, 4 and 8; 128 parts of 4 rows 58 in one, 51.5 in two.  With 8
+// parts (16 of 8 rows, 32 of 4) and less the second arrival costs more, 1 us.
+constexpr int kManyParts = 8, kGroup = 4;
 // Tiles that a unit counts beside its own, us of (48 sequences up to 2304 keys
 // bf16, the same in e4m3, 16 of a window of 1024 keys, 64 of 8192 keys e4m3,
 // one of 8192): 0: 32.0 / 27.7 / 17.9 / 65 / 11.7; 4: 28.1 / 23.0 / 14.0 / 61.6 / 12.9;
@@ -559,19 +561,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
         // the threads left over take every other part, and meet in LDS.
         int sets = 1;
         while (sets < 16 && rows <= 8 / sets) sets *= 2;
-        int size = 1;
-        while (last - first + 1 > kManyParts * sets && size * size < last - first + 1) size *= 2;
-        int level = whole ? 2 : size > 1 ? 0 : 1;
+        int left = whole ? 0 : last - first + 1, part_at = (int)w - first, apart = 0;      // parts; this workgroup's; 2^apart workgroups from one to the next
 #pragma unroll 1
-        for (; level < 2; ++level) {
-            const bool all = level == 1;
-            const int group = all ? 0 : ((int)w - first) / size;
-            const int from = first + group * size, step = all ? size : 1;                      // parts from, from + step, ..
-            const int n = all ? (last - first) / size + 1 : min(size, last - from + 1);
+        for (int turn = 1; left; turn += 2) {
+            const bool all = left <= kManyParts * sets;
+            int bits = 1;       // of a group
+            while ((1 << 2 * bits) < left && (1 << bits) < kGroup * sets) ++bits;
+            const int group = all ? 0 : part_at >> bits, n = all ? left : min(1 << bits, left - (group << bits));
+            const int from = first + ((group << bits) << apart);
             // (a workgroup can be the last of one unit and the first of another)
-            unsigned* const counter = p.cnt + (size_t)from * kCtrWords + (all ? 0 : group ? 2 : 1);
+            unsigned* const counter = p.cnt + (size_t)from * kCtrWords + (all ? 0 : group ? turn + 1 : turn);
             if (!arrive_last(counter, n, tid, &s_prev)) break;
-            auto slot_of = [&](int k) { const int x = from + k * step; return 2 * x + (x == first && (uint32_t)x * share < unit ? 1 : 0); };
+            auto slot_of = [&](int k) { const int x = from + (k << apart); return 2 * x + (x == first && (uint32_t)x * share < unit ? 1 : 0); };
             const int width = 16 / sets;       // rows that the threads hold at a time
             const int set = (tid >> 4) / width;
 #pragma unroll 1
@@ -641,6 +642,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
                     else keep(slot_of(0), r, ch, o, m, l);
                 }
             }
+            part_at = group;
+            apart += bits;
+            left = all ? 0 : (left + (1 << bits) - 1) >> bits;
         }
         __syncthreads();       // LDS is free for the next unit
         pos = unit + (uint32_t)(tile + tiles);
