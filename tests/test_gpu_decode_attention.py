@@ -118,6 +118,14 @@ def test_many_parts(q4, ws, T, Hq, Hk, e4m3):
     assert torch.equal(check(q4, ws, p).view(torch.int16), y.view(torch.int16))
 
 
+@pytest.mark.parametrize("T,G", [(1, 1), (3, 2), (2, 6), (8, 4), (16, 4)])
+def test_one_unit_over_all_workgroups(q4, ws, T, G):
+    """One sequence and key head: hundreds of parts of 1 to 32 rows (or two units of them)."""
+    p = problem([70001], T, G, 1, 64, 64, 23)
+    y = check(q4, ws, p)
+    assert torch.equal(run(q4, ws, *p).view(torch.int16), y.view(torch.int16))
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("B,T,Hq,Hk", [(70, 40, 2, 1), (64, 9, 8, 2), (200, 2, 32, 2)])
 def test_many_rows_of_many_sequences(q4, ws, B, T, Hq, Hk, e4m3):
