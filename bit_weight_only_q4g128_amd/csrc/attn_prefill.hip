@@ -53,9 +53,13 @@ constexpr int kWaveRows = 32;
 // 507 (and 64 for the window where 4 took 49), 2 took 652.
 constexpr int kWaves = 4;
 // Workgroups that share a CU.  Registers set them; with heads of 64 columns a
-// third one pays though five registers are then spilled (window: 50 -> 43 us,
-// long prompts of such heads 182 -> 171).
+// third one pays (window: 50 -> 43 us, long prompts of such heads 182 -> 171).
 constexpr int workgroups(int D) { return D == 64 ? 3 : 2; }
+// A score's exponent is z c - m c, rounded once, from m c rounded: off by half
+// a step of m c, alike for all of a row's keys, which is 2^-13 below this size
+// of m c and would be more than fp32's exponents hold from 2^31 on. From here on
+// it is (z - m) c instead.
+constexpr float kLarge = 0x1p12f;
 
 struct PrefillParams {
     PrefillArgs a;
@@ -265,9 +269,22 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
         for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j >> 4][j & 15]);
         return top;
     };
+    // what a row's settled scores, times c, have subtracted (0 before its first key)
+    auto taken = [&] {
+        const float mc = m * p.c;
+        return fabsf(mc) < kLarge ? mc : 0.f;
+    };
+    // A score of a row whose maximum is large: subtracted here.  Where the
+    // maximum leaves fp32's range it is infinite: a row of infinity is NaN, and
+    // of -infinity alone every weight is 0.
+    auto reduced = [&](float x) {
+        const float mc = m * p.c;
+        if (fabsf(mc) < kLarge) return x;
+        return mc == -__builtin_inff() ? x * p.c : x - (mc == __builtin_inff() ? __builtin_nanf("") : m);
+    };
     // the scores' weights into the sums and outputs, with the values of step i
     auto outputs = [&](const f32x16 (&z)[2], int i) {
-        const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
+        const float mc = taken();
         const uint32_t at = base + (uint32_t)(i & 1) * L::kStage + L::kBytes + v_read;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -310,6 +327,10 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) o[t] *= x;
         }
+        if (__any(fabsf(m * p.c) >= kLarge && m > -__builtin_inff())) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j >> 4][j & 15] = reduced(z[j >> 4][j & 15]);
+        }
     };
     // One step: this step's weights and outputs beside the next one's scores,
     // in this order, which nothing changes: a matrix instruction, the fragment of
@@ -322,7 +343,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
         constexpr int kAhead = D == 64 ? 2 : 4;      // fragments on their way (more registers with three workgroups a CU: 1 % slower)
         const uint32_t k_at = base + (uint32_t)((i + 1) & 1) * L::kStage + k_read;
         const uint32_t v_at = base + (uint32_t)(i & 1) * L::kStage + L::kBytes + v_read;
-        const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
+        const float mc = taken();
         u32x4 f[2 * kN], w[4];
         float e[16][2], top[2] = {-__builtin_inff(), -__builtin_inff()};
         auto read = [&](auto at) {
@@ -407,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
         // Rare: where some rows see keys that others do not, some values are
         // infinities or NaNs.  Those values alone, which were left out above,
         // key by key into the rows that see them.
-        const float mc = m == -__builtin_inff() ? 0.f : m * p.c;
+        const float mc = taken();
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
             if (!partly(i)) continue;
@@ -430,7 +451,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
                 }
                 float w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf((k & 1) ? z[8 + j] : z[j], p.c, -mc));
+                for (int j = 0; j < 8; ++j) w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(reduced((k & 1) ? z[8 + j] : z[j]), p.c, -mc));
                 const u32x4 pk{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
 #pragma unroll 1
                 for (int j = 0; j < 16; ++j) {
