@@ -916,6 +916,13 @@ def _kv_cache(cache, index: int, Hk: int, D: int):
     return _KV_CACHE(kp, vp, ksp, vsp, pages, page_size), page_size
 
 
+def _rotated(out, name: str, shape, index: int, x, stride: int):
+    """A contiguous output for the heads x.  The library takes an output at x's
+    address for x itself, its tokens `stride` elements apart."""
+    if _tensor(out, name, _U16, shape, index) == x.data_ptr() and stride != shape[1] * shape[2]:
+        raise ValueError(f"{name} begins where {name[0]} does, whose tokens lie apart: in place is {name[0]} itself")
+
+
 def rope_cache(q, k, v=None, positions=None, inv_freq=None, q_norm=None, k_norm=None, eps: float = 1e-6, interleaved: bool = False,
                cache=None, slots=None, q_out=None, k_out=None):
     """q's and k's heads normalised (q_norm, k_norm: bf16 weights [D], or None)
@@ -951,11 +958,11 @@ def rope_cache(q, k, v=None, positions=None, inv_freq=None, q_norm=None, k_norm=
     if q_out is None:
         q_out = q.new_empty((T, Hq, D))
     elif q_out is not q:
-        _tensor(q_out, "q_out", _U16, (T, Hq, D), index)
+        _rotated(q_out, "q_out", (T, Hq, D), index, q, qs)
     if k_out is True or (k_out is None and cache is None):
         k_out = k.new_empty((T, Hk, D))
     elif k_out is not None and k_out is not k:
-        _tensor(k_out, "k_out", _U16, (T, Hk, D), index)
+        _rotated(k_out, "k_out", (T, Hk, D), index, k, ks)
     _enqueue(index, lib.q4_rope_cache, q.data_ptr(), k.data_ptr(), vp, T, Hq, Hk, D, qs, ks, vs,
              _optional(q_norm, "q_norm", _U16, (D,), index), _optional(k_norm, "k_norm", _U16, (D,), index), eps, pp, fp, rot,
              1 if interleaved else 0, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), cp, sp)
