@@ -27,6 +27,7 @@ bool heads_ok(int Hq, int Hk, int D) {
 }
 bool stride_ok(int64_t stride, int heads, int D) { return stride >= (int64_t)heads * D && stride <= kMaxStride && stride % 8 == 0; }
 bool positive(float f) { return f > 0.f && f < __builtin_huge_valf(); }
+bool scale_ok(float f) { return f > 0.f && f <= 0x1p127f; }      // times log2 e it is finite
 
 // Rows of `width` elements, `stride` elements from one to the next.
 struct Rows {
@@ -121,7 +122,7 @@ int q4_attention_decode(const uint16_t* q, int B, int T, int Hq, int Hk, int D, 
                         uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !cache || !table || !lengths || !y || !workspace) return Q4_EINVAL_PTR;
     if (B < 1 || B > q4::kMaxSequences || T < 1 || T > kMaxNew || !heads_ok(Hq, Hk, D) || !stride_ok(q_stride, Hq, D)) return Q4_EINVAL_SHAPE;
-    if (width < 1 || window < 0 || !positive(scale)) return Q4_EINVAL_SHAPE;
+    if (width < 1 || window < 0 || !scale_ok(scale)) return Q4_EINVAL_SHAPE;
     q4::Cache c{};
     CacheRanges cr{};
     const int rc = check_cache(cache, Hk, D, &c, &cr);
@@ -151,7 +152,7 @@ int q4_attention_prefill(const uint16_t* q, int T, const uint16_t* k, const uint
     if (!q || !k || !v || !starts || !y) return Q4_EINVAL_PTR;
     if (T < 1 || T > kMaxTokens || S < 1 || S > kMaxTokens || B < 1 || B > q4::kMaxSequences || !heads_ok(Hq, Hk, D)) return Q4_EINVAL_SHAPE;
     if (!stride_ok(q_stride, Hq, D) || !stride_ok(k_stride, Hk, D) || !stride_ok(v_stride, Hk, D)) return Q4_EINVAL_SHAPE;
-    if (window < 0 || !positive(scale)) return Q4_EINVAL_SHAPE;
+    if (window < 0 || !scale_ok(scale)) return Q4_EINVAL_SHAPE;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(key_starts, 4) || !aligned(y, 16))
         return Q4_EALIGN;
     const Rows out{y, T, (int64_t)Hq * D, (int64_t)Hq * D};

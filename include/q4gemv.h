@@ -592,13 +592,14 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
  * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
  * Keys and values that a row does not see have no effect on it, whatever they
- * hold.  Scores, softmax and sums are fp32 (a score that leaves its range is
- * infinite); a weight (times an 8-bit value's scale) is rounded to bf16 before it
- * multiplies its value.
+ * hold.  Scores, softmax and sums are fp32 (a score that leaves its range, before
+ * its scales or after them, is infinite); a weight (times an 8-bit value's scale)
+ * is rounded to bf16 before it multiplies its value.
  *
  * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
  * 2^24, and B * Hk * (ceil(width * page_size / 32) + 8), times ceil(T * Hq / Hk / 32)
- * where T * Hq / Hk is above 16, below 2^31; scale finite and > 0; window >= 0.
+ * where T * Hq / Hk is above 16, below 2^31; 0 < scale <= 2^127 (a k_scale's product
+ * with it as well); window >= 0.
  * Alignment: q and y 16 bytes, table, lengths, n_new 4.
  * workspace: at least q4_attention_decode_workspace_bytes, 256-byte aligned,
  * zero-filled before its first use; its first 64 KiB are arrival counters that

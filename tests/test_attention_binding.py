@@ -45,3 +45,12 @@ def test_outputs_at_an_inputs_address(launched, interleaved):
     one = base.view(-1)[:q.numel()].view(q.shape)
     assert q4.rope_cache(q, k, q_out=one)[0] is one
     assert len(launched) == 3
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127 * (1 + 2.0 ** -23), 2.4e38, 3e38, 3.4028234e38])
+def test_scale_past_its_limit(scale):
+    """scale * log2 e is an fp32 number."""
+    from test_abi_attention import ESHAPE, decode, prefill
+    assert decode(scale=scale) == ESHAPE
+    assert decode(scale=scale, ks=(1 << 40) * 23, vs=(1 << 40) * 24) == ESHAPE
+    assert prefill(scale=scale) == ESHAPE

@@ -148,3 +148,17 @@ def test_infinite_scores(q4, call, D, window, key, scale):
             continue
         want = ve[even].mean(0)
         within(y[t, 0], want, 2.0 ** -8 * np.abs(want) + 2.0 ** -22 * len(even) * np.abs(ve[even]).mean(0), f"row {t}")
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** -126, 2.0 ** -149])
+def test_scale_at_its_limits(q4, call, scale):
+    """Queries of 0 give every key the score 0, whatever the scale."""
+    n, D = 70, 64
+    v = problem(n, n, 1, 1, D, 3)[1]
+    k = torch.randn(n, 1, D, device="cuda").to(torch.bfloat16)
+    y = values(CALLS[call](q4, torch.zeros(n, 1, D, dtype=torch.bfloat16, device="cuda"), k, v, scale, 0))
+    ve = values(v)[:, 0]
+    for t in range(n):
+        want = ve[:t + 1].mean(0)
+        within(y[t, 0], want, 2.0 ** -8 * np.abs(want) + 2.0 ** -22 * (t + 1) * np.abs(ve[:t + 1]).mean(0), f"row {t}")
