@@ -105,15 +105,18 @@ __global__ __launch_bounds__(kThreads) void rope_cache_kernel(const RopeParams p
         for (int j = 0; j < 4; ++j) h[2 * j] = bf16lo(x[j]), h[2 * j + 1] = bf16hi(x[j]);
         if (!is_v) {
             if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
-                float ss = 0.f;
+                float ss = 0.f, eps = a.eps;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[j], h[j], ss);
                 ss = group_sum(ss, kLanes);
-                float eps = a.eps;
-                if (!(ss < 0x1p126f)) {      // rare: squares that leave fp32's range; eps is nothing beside them
-                    ss = eps = 0.f;
+                const float mean = __builtin_fmaf(ss, 1.0f / D, eps);
+                // rare: a mean near the ends of fp32's range, whose squares may have left it or
+                // lost bits; head and eps are scaled, which the quotient does not see
+                if (!(mean < 0x1p120f) || mean < 0x1p-80f) {
+                    const float f = mean < 0x1p-80f ? 0x1p70f : 0x1p-70f;
+                    ss = 0.f, eps = eps * f * f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) h[j] *= 0x1p-70f, ss = __builtin_fmaf(h[j], h[j], ss);
+                    for (int j = 0; j < 8; ++j) h[j] *= f, ss = __builtin_fmaf(h[j], h[j], ss);
                     ss = group_sum(ss, kLanes);
                 }
                 const float inv = rsqrtf(__builtin_fmaf(ss, 1.0f / D, eps));
