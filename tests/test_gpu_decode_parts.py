@@ -1,0 +1,62 @@
+"""attention_decode's parts one by one, through the binding: that each tile of
+keys, each workgroup's part and each group of a join arrives once and where it
+belongs.  Inputs and tolerances: attention_parts; that they show
+what they are meant to: test_attention_parts."""
+import numpy as np
+import pytest
+import torch
+
+from attention_parts import Planted, counted, counted_check, counted_want
+from attention_util import values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q4():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_weight_only_q4g128_amd as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def ws():
+    return torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")
+
+
+def on_gpu(q, cache, table, lens):
+    return q.cuda(), tuple(t.cuda() for t in cache), table.cuda(), lens.cuda()
+
+
+# one unit over all workgroups, with joins in one to four turns (1 to 32 rows, or
+# two units of them); units that share workgroups; ragged ones
+LENGTHS = [([70001], 1, 1, 1), ([70001], 3, 2, 1), ([70001], 2, 6, 1), ([70001], 8, 4, 1), ([70001], 16, 4, 1), ([20000], 1, 2, 2),
+           ([9000, 14000, 33, 16000, 4500], 1, 12, 1), ([9000, 14000, 70, 16000, 4500], 8, 6, 2), ([9000, 1100, 4097, 300], 1, 4, 2),
+           ([1300] * 3 + [40] * 70 + [5000, 700], 1, 4, 2), ([3000] * 64 + [40000], 5, 4, 1)]
+
+
+@pytest.mark.parametrize("lengths,T,G,Hk", LENGTHS)
+@pytest.mark.parametrize("D,P", [(64, 64), (128, 16)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_tile_counts(q4, ws, lengths, T, G, Hk, D, P, e4m3):
+    q, cache, table, lens = on_gpu(*counted(lengths, T, G * Hk, Hk, D, P, e4m3))
+    n_new = [1 + (3 * b) % T for b in range(len(lengths))]
+    for new, window in ((None, 0), (n_new, 0), (None, 1000)):
+        dev = None if new is None else torch.tensor(new, dtype=torch.int32, device="cuda")
+        y = q4.attention_decode(q, cache, table, lens, dev, 1.0, window, workspace=ws)
+        assert not ws[:65536].any()
+        counted_check(values(y), counted_want(lengths, new, T, G * Hk, Hk, D, window))
+
+
+@pytest.mark.parametrize("lengths,T,G,Hk", [c for c in LENGTHS if min(c[0]) > 32 * c[1] * c[2] + c[1]])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_tile_decides(q4, ws, lengths, T, G, Hk, e4m3):
+    p = Planted(lengths, T, G * Hk, Hk, 64, 64, e4m3, "cuda")
+    q, table, lens = p.q.cuda(), p.table.cuda(), p.lens.cuda()
+    for s in range(p.turns):
+        p.plant(s)
+        y = q4.attention_decode(q, p.cache, table, lens, workspace=ws)
+        p.check(y, f"turn {s}")
+        p.lift()
+    assert not ws[:65536].any()
