@@ -15,6 +15,14 @@ Planted.  Key j of a row is 8 times its query: it outweighs all others by e^40 (
 condition that is checked), and the row is value j, which bf16 holds.  Every tile
 of 32 keys has its turn.  A part that is lost or joined into another row is
 another value altogether.
+
+Marked.  A table of 2^24 keys that names one page of zeros everywhere but at
+chosen places, each of which has a page of its own, of keys that outweigh those
+zeros by e^14, and values of 1, 2 or 4 in one column: a column counts its marked
+pages, up to 16 of them, so that one that is lost, doubled or read with another
+page's keys, values or scales is 2.7 % of its column or more.  Marked keys weigh 1,
+exactly, and the others have no value; the sum of up to 2^24 weights is off by the
+weights a lane adds, some thousand of 2^-24 each, below 2^-10.
 """
 import numpy as np
 import torch
@@ -170,3 +178,92 @@ class Planted:
         # the others together are below n e^-40 4; the value is a bf16 number
         bad = ~((y - want).abs() <= 2.0 ** -10 * want.abs() + 1e-10)
         assert not bad.any(), f"{what}: {int(bad.any(-1).sum())} rows off, first {bad.any(-1).nonzero()[0].tolist()}"
+
+
+# ---------------------------------------------------------------------------
+# marked
+# ---------------------------------------------------------------------------
+WORKGROUPS, OWN = 512, 8         # of a decode call of many tiles; places that a unit takes beside its tiles
+
+
+def list_pages(D, R):
+    """Pages that a workgroup's list holds: 4 waves' outputs of 16 or 32 rows, in whole steps of 128 keys."""
+    return 4 * (16 if R <= 16 else 32) * (D + 4) // 8 * 8
+
+
+def segments(n, Hk, R):
+    """(first tile, tiles) of every workgroup's part of a unit, one sequence of n keys."""
+    Z = -(-R // 32)
+    tiles = -(-n // TILE)
+    unit = tiles + OWN
+    total = Hk * Z * unit
+    share = -(-total // WORKGROUPS)
+    out = []
+    for start in range(0, total, share):
+        pos, stop = start, min(total, start + share)
+        while pos < stop:
+            at = pos % unit
+            first, last = max(at, OWN), min(unit, at + stop - pos)
+            if last > first:
+                out.append((first - OWN, last - first))
+            pos += min(unit - at, stop - pos)
+    return out
+
+
+def places(n, Hk, R, D, P, most):
+    """Page numbers of the sequence where a workgroup's part or a list of its
+    pages begins or ends, those of up to `most` segments; how many lists end
+    inside a segment."""
+    parts = segments(n, Hk, R)
+    hold, ends, found = list_pages(D, R), 0, set()
+    chosen = parts if len(parts) <= most else [parts[i * (len(parts) - 1) // (most - 1)] for i in range(most)]
+    whole = n // P
+    for first, tiles in chosen:
+        page, last = first * TILE // P, ((first + tiles) * TILE - 1) // P
+        found |= {page, last}
+        while (page := page + hold) <= last:
+            found |= {page - 1, page, page + 1}
+            ends += 1
+    return sorted(x for x in found if x < whole), ends
+
+
+LOUD = 14.0                      # of a marked key's score, 3.5 * 4 (e4m3 and bf16 numbers)
+
+
+def marked(n, T, Hq, Hk, D, P, e4m3, at):
+    """(q, cache, table, lengths) on the CPU, pages `at` of the table marked."""
+    pages = 1 + len(at)
+    value = 2.0 ** (torch.arange(len(at)) // D % 3)
+    q = torch.zeros(1, T, Hq, D, dtype=torch.bfloat16)
+    q[..., 0] = 4.0
+    k, v = torch.zeros(pages, Hk, P, D), torch.zeros(pages, Hk, P, D)
+    k[1:, :, :, 0] = 3.5
+    m = torch.arange(len(at))
+    v[1 + m, :, :, m % D] = 1.0 if e4m3 else value[:, None, None]
+    table = torch.zeros(1, -(-n // P), dtype=torch.int32)
+    table[0, torch.tensor(at)] = (1 + m).to(torch.int32)
+    lens = torch.tensor([n], dtype=torch.int32)
+    if not e4m3:
+        return q, (k.to(torch.bfloat16), v.to(torch.bfloat16)), table, lens
+    ks, vs = torch.full((pages, Hk, P), 0.25), torch.full((pages, Hk, P), 16.0)
+    ks[1:], vs[1:] = 1.0, value[:, None, None]
+    return q, (k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), ks, vs), table, lens
+
+
+def marked_want(n, T, D, P, at, counts=None):
+    """fp64 [T, D]; counts: how often each marked page is taken (1)."""
+    m = np.arange(len(at))
+    counts = np.ones(len(at)) if counts is None else counts
+    loud = np.exp(LOUD)
+    y = np.zeros((T, D))
+    for i in range(T):
+        end = n - T + i + 1
+        l = loud * P * counts.sum() + (end - P * len(at))
+        np.add.at(y[i], m % D, loud * P * counts * 2.0 ** (m // D % 3) / l)
+    return y
+
+
+def marked_check(y, want):
+    assert y.shape == want.shape
+    bad = ~(np.abs(y - want) <= (2.0 ** -8 + 2.0 ** -9) * want)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} off, first {tuple(np.argwhere(bad)[0])}: {y[bad][0]!r}, not {want[bad][0]!r}"

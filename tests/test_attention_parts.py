@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from attention_parts import TILE, Planted, counted, counted_check, counted_want
+from attention_parts import TILE, Planted, counted, counted_check, counted_want, list_pages, marked, marked_check, marked_want, places, segments
 
 
 def rounded(y):
@@ -98,3 +98,38 @@ def test_planted_shows_a_part(e4m3):
         p.lift()
     assert len(seen) >= (n - T) // TILE
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, p.cache))
+
+
+REFILLED = [(64, 3, 1, 1, 16), (128, 8, 1, 1, 16), (64, 8, 2, 9, 16), (64, 8, 1, 1, 32)]
+
+
+@pytest.mark.parametrize("D,Hk,G,T,P", REFILLED)
+def test_marked_shows_a_list(D, Hk, G, T, P):
+    n = (1 << 24) - 5
+    at, ends = places(n, Hk, G * T, D, P, 8 * D // 5)
+    assert ends > D and 4 * D < len(at) <= 16 * D
+    parts = segments(n, Hk, G * T)
+    assert sum(t for _, t in parts) == Hk * -(-G * T // 32) * -(-n // TILE)
+    want = marked_want(n, T, D, P, at)
+    marked_check(rounded(want), want)
+    at = np.array(at)
+    # one marked page lost or taken twice; a list of pages lost, or the one before it in its place
+    first, tiles = max(parts, key=lambda s: s[1])
+    page, hold = first * TILE // P, list_pages(D, G * T)
+    for keep in [np.where(at == at[len(at) // 2], x, 1.0) for x in (0.0, 2.0)] + [np.where((at >= page + hold) & (at < page + 2 * hold), 0.0, 1.0),
+                                                                                 np.where((at >= page) & (at < page + hold), 2.0, 1.0)]:
+        assert (keep != 1).any()
+        with pytest.raises(AssertionError):
+            marked_check(rounded(marked_want(n, T, D, P, at, keep)), want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_marked_inputs(e4m3):
+    """The inputs give what is wanted of them."""
+    n, T, Hq, Hk, D, P = 40000 - 5, 2, 4, 2, 64, 16
+    at = [0, 3, 4, 900] + list(range(1000, 1140))
+    q, cache, table, _ = marked(n, T, Hq, Hk, D, P, e4m3, at)
+    for h in range(Hk):
+        k, v = gathered(cache, table[0], n, h)
+        y, _, _ = oracle.attend(q[0, :, 2 * h].double().numpy(), k, v, n - T + 1 + np.arange(T), 1.0)
+        assert np.allclose(y, marked_want(n, T, D, P, at), rtol=1e-12)

@@ -1,12 +1,12 @@
 """attention_decode's parts one by one, through the binding: that each tile of
-keys, each workgroup's part and each group of a join arrives once and where it
-belongs.  Inputs and tolerances: attention_parts; that they show
+keys, each workgroup's part, each group of a join and each list of pages arrives
+once and where it belongs.  Inputs and tolerances: attention_parts; that they show
 what they are meant to: test_attention_parts."""
 import numpy as np
 import pytest
 import torch
 
-from attention_parts import Planted, counted, counted_check, counted_want
+from attention_parts import Planted, counted, counted_check, counted_want, list_pages, marked, marked_check, marked_want, places, segments
 from attention_util import values
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,18 @@ def test_every_tile_decides(q4, ws, lengths, T, G, Hk, e4m3):
         p.check(y, f"turn {s}")
         p.lift()
     assert not ws[:65536].any()
+
+
+@pytest.mark.parametrize("D,Hk,G,T,P,e4m3", [(64, 3, 1, 1, 16, False), (128, 8, 1, 1, 16, False), (64, 8, 2, 9, 16, False),
+                                             (64, 8, 1, 1, 32, False), (64, 4, 1, 1, 16, True), (128, 8, 1, 1, 16, True)])
+def test_every_list_of_pages(q4, ws, D, Hk, G, T, P, e4m3):
+    """More pages to a workgroup than its list holds: those at the ends of its
+    lists and of its part, each with keys and values of its own."""
+    n = (1 << 24) - 5
+    assert min(t for _, t in segments(n, Hk, G * T)[:8]) * 32 > list_pages(D, G * T) * P
+    at, ends = places(n, Hk, G * T, D, P, 8 * D // 5)
+    assert ends > D
+    y = q4.attention_decode(*on_gpu(*marked(n, T, G * Hk, Hk, D, P, e4m3, at)), scale=1.0, workspace=ws)
+    want = marked_want(n, T, D, P, at)
+    for h in range(G * Hk):
+        marked_check(values(y)[0, :, h], want)
