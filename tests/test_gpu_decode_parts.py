@@ -1,13 +1,15 @@
 """attention_decode's parts one by one, through the binding: that each tile of
 keys, each workgroup's part, each group of a join and each list of pages arrives
 once and where it belongs.  Inputs and tolerances: attention_parts; that they show
-what they are meant to: test_attention_parts."""
+what they are meant to: test_attention_parts.  And infinities and NaNs, row by row
+of every sequence and head."""
 import numpy as np
 import pytest
 import torch
 
 from attention_parts import Planted, counted, counted_check, counted_want, list_pages, marked, marked_check, marked_want, places, segments
 from attention_util import values
+from test_gpu_decode_attention import problem
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +77,64 @@ def test_every_list_of_pages(q4, ws, D, Hk, G, T, P, e4m3):
     want = marked_want(n, T, D, P, at)
     for h in range(G * Hk):
         marked_check(values(y)[0, :, h], want)
+
+
+@pytest.mark.parametrize("T,window", [(1, 0), (1, 50), (4, 0), (4, 50), (64, 0), (40, 20)])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Hq,Hk", [(4, 1), (6, 2)])
+def test_keys_that_are_no_numbers(q4, ws, T, window, e4m3, Hq, Hk):
+    """NaNs in keys at the ends of what rows see: every head of every row that
+    sees one is NaN, every other row what it is without."""
+    lengths, P = [200, 161, 300, 75], 16
+    p = problem(lengths, T, Hq, Hk, 128, P, 30, e4m3)
+    q, cache, table, lens = on_gpu(*p)
+    call = lambda: q4.attention_decode(q, cache, table, lens, window=window, workspace=ws)  # noqa: E731
+    clean = call()
+    spots = {b: [n - 1] + ([n - window - 1] if window else [n - 40]) for b, n in enumerate(lengths)}
+    for b, js in spots.items():
+        for j in js:
+            page, at = int(p[2][b, j // P]), j % P
+            if e4m3:
+                cache[0].view(torch.uint8)[page, :, at, 7] = 0x7F
+            else:
+                cache[0][page, :, at, 7] = float("nan")
+    y = call()
+    for b, n in enumerate(lengths):
+        for i in range(T):
+            end = n - T + i + 1
+            if any(max(0, end - window if window else 0) <= j < end for j in spots[b]):
+                assert torch.isnan(y[b, i]).all(), (b, i)
+            else:
+                assert torch.equal(y[b, i], clean[b, i]), (b, i)
+
+
+@pytest.mark.parametrize("T,window", [(1, 0), (4, 0), (4, 50), (64, 0), (40, 20)])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,Hq,Hk", [(128, 4, 1), (64, 6, 2)])
+def test_values_that_are_no_numbers(q4, ws, T, window, e4m3, D, Hq, Hk):
+    """An infinity or NaN in one column of a value, each sequence and head with
+    columns of its own: that column of the rows that see it, and nothing else."""
+    lengths, P, G = [200, 161, 300, 75], 16, Hq // Hk
+    p = problem(lengths, T, Hq, Hk, D, P, 31, e4m3)
+    q, cache, table, lens = on_gpu(*p)
+    call = lambda: q4.attention_decode(q, cache, table, lens, window=window, workspace=ws)  # noqa: E731
+    clean = call()
+    want = clean.clone()
+    for b, n in enumerate(lengths):
+        js = sorted({n - 1, n - 2, max(n - T - 1, 0), max(n - T - (window or 35), 0), max(n - (window or 50) - 2, 0)})
+        for h in range(Hk):
+            for x, j in enumerate(js):
+                page, at, col = int(p[2][b, j // P]), j % P, (11 * b + 5 * h + 3 * x) % D
+                odd = [float("inf"), float("nan"), float("-inf")][(b + h + x) % 3]
+                if e4m3:
+                    odd = float("nan")
+                    cache[1].view(torch.uint8)[page, h, at, col] = 0x7F
+                else:
+                    cache[1][page, h, at, col] = odd
+                for i in range(T):
+                    end = n - T + i + 1
+                    if max(0, end - window if window else 0) <= j < end:
+                        want[b, i, h * G:(h + 1) * G, col] = odd
+    y = call()
+    same = (y == want) | (torch.isnan(y) & torch.isnan(want))
+    assert same.all(), (~same).nonzero()[:4].tolist()
