@@ -70,6 +70,29 @@ constexpr int kAhead = 4;                    // parts that a thread has in fligh
 // 57 in groups of 4, 4 and 8; 128 parts of 4 rows 58 in one, 51.5 in two.  With 8
 // parts (16 of 8 rows, 32 of 4) and less the second arrival costs more, 1 us.
 constexpr int kManyParts = 8, kGroup = 4;
+// parts of a group, as a power of two, where `left` parts are joined by `sets` sets of threads
+__host__ __device__ constexpr int group_bits(int left, int sets) {
+    int bits = 1;
+    while ((1 << 2 * bits) < left && (1 << bits) < kGroup * sets) ++bits;
+    return bits;
+}
+// Counters of a workgroup that a join of up to kMaxWgs parts reaches: the last
+// turn's, and two of each turn before it (the first group's, whose workgroup
+// may also be the last of the unit before, and another group's).
+constexpr int join_counters() {
+    int most = 1;
+    for (int sets = 1; sets <= 16; sets *= 2)
+        for (int parts = 1; parts <= kMaxWgs; ++parts) {
+            int words = 1;
+            for (int left = parts; left > kManyParts * sets; words += 2) {
+                const int bits = group_bits(left, sets);
+                left = (left + (1 << bits) - 1) >> bits;
+            }
+            most = words > most ? words : most;
+        }
+    return most;
+}
+static_assert(join_counters() == 7 && join_counters() <= kCtrWords, "a workgroup's counters are one line's");
 // Tiles that a unit counts beside its own, us of (48 sequences up to 2304 keys
 // bf16, the same in e4m3, 16 of a window of 1024 keys, 64 of 8192 keys e4m3,
 // one of 8192): 0: 32.0 / 27.7 / 17.9 / 65 / 11.7; 4: 28.1 / 23.0 / 14.0 / 61.6 / 12.9;
@@ -566,8 +589,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
 #pragma unroll 1
         for (int turn = 1; left; turn += 2) {
             const bool all = left <= kManyParts * sets;
-            int bits = 1;       // of a group
-            while ((1 << 2 * bits) < left && (1 << bits) < kGroup * sets) ++bits;
+            const int bits = group_bits(left, sets);
             const int group = all ? 0 : part_at >> bits, n = all ? left : min(1 << bits, left - (group << bits));
             const int from = first + ((group << bits) << apart);
             // (a workgroup can be the last of one unit and the first of another)
