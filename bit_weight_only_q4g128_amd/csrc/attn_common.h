@@ -63,13 +63,17 @@ __device__ __forceinline__ float sum_xor16(float v) {
 // a lane counts a run of ceil(B / 64) <= 64 sequences, the wave sums the runs up
 // to each lane, and the run that holds a position is then spread over the
 // lanes the same way.
+// All of this needs the whole wave: a scan reads its neighbours' registers, and
+// a lane that is switched off (a branch or the right side of && that only some
+// lanes reach) is read as it last was, or not at all, so that the place found
+// can lie outside the work.  Lanes without a sequence count 0.
 // ---------------------------------------------------------------------------
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
     return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
-// Inclusive prefix sum over the 64 lanes (shifts within rows of 16, then the
-// row totals broadcast forward).
+// Inclusive prefix sum over the 64 lanes, all of them active (shifts within rows
+// of 16, then the row totals broadcast forward).
 __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     v = dpp_add<0x111>(v);
     v = dpp_add<0x112>(v);
@@ -85,6 +89,7 @@ struct Runs {
     uint32_t upto;      // units up to this lane's run and with it
     uint32_t total;     // of all
 };
+// (the whole wave)
 template <typename Count>
 __device__ __forceinline__ Runs count_runs(int B, int lane, Count count) {
     Runs r{(B + 63) >> 6, 0, 0};
@@ -102,7 +107,7 @@ struct Place {
     int seq;         // the sequence that holds a position
     uint32_t at;     // units before the position inside it
 };
-// pos < r.total
+// pos < r.total, the same in all lanes (the whole wave)
 template <typename Count>
 __device__ __forceinline__ Place find_place(const Runs& r, int B, int lane, uint32_t pos, Count count) {
     const int owner = __builtin_ctzll(__ballot(r.upto > pos));
