@@ -281,9 +281,27 @@ __device__ __forceinline__ void weights(State<D, NT>& st, float (&z)[NT][8]) {
         }
         const float m = st.m[n] == -__builtin_inff() ? 0.f : st.m[n];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            z[n][j] = __builtin_amdgcn_exp2f(z[n][j] - m);
-            st.l[n] += z[n][j];
+        for (int j = 0; j < 8; ++j) z[n][j] = __builtin_amdgcn_exp2f(z[n][j] - m);
+    }
+}
+
+// The sum of the weights.  They are rounded to bf16, the products' operands, and
+// the sum is of the rounded ones, so that a row is a mean of its values: equal
+// values are met exactly, where the sum of the others was off by up to 2^-8.  With
+// 8-bit values, themselves up to 2^-4 off, a weight times its value's scale is
+// rounded, and the sum is of the weights before: dividing each by its scale
+// again would be two more operations a key and row.
+template <int D, bool kE4m3, int NT>
+__device__ __forceinline__ void add_up(State<D, NT>& st, const float (&z)[NT][8], const bf16x8 (&pr)[NT]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if constexpr (kE4m3) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st.l[n] += z[n][j];
+        } else {
+            const u32x4 w = __builtin_bit_cast(u32x4, pr[n]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st.l[n] = dot2(w[j], 0x3F803F80u, st.l[n]);
         }
     }
 }
@@ -458,6 +476,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(const DecodePa
                 weights<D, NT>(st, z);
                 bf16x8 pr[NT];
                 values.template operands<NT>(pr, z, edge);
+                add_up<D, kE4m3, NT>(st, z, pr);
                 // (new tokens are at most 64, so that at most one step of a wave lies
                 // where the keys that rows see begin, and one where they end)
                 const bool partly = sp.n > 1 && (k0 + kTile > first_end || k0 < last_low);

@@ -594,7 +594,8 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * Keys and values that a row does not see have no effect on it, whatever they
  * hold.  Scores, softmax and sums are fp32 (a score that leaves its range, before
  * its scales or after them, is infinite); a weight (times an 8-bit value's scale)
- * is rounded to bf16 before it multiplies its value.
+ * is rounded to bf16 before it multiplies its value, and, where values are bf16,
+ * before it is summed, so that a row is a mean of its values.
  *
  * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
  * 2^24, and B * Hk * (ceil(width * page_size / 32) + 8), times ceil(T * Hq / Hk / 32)

@@ -138,3 +138,24 @@ def test_values_that_are_no_numbers(q4, ws, T, window, e4m3, D, Hq, Hk):
     y = call()
     same = (y == want) | (torch.isnan(y) & torch.isnan(want))
     assert same.all(), (~same).nonzero()[:4].tolist()
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D", [(1, 16, 4, 128), (5, 8, 2, 64), (8, 6, 1, 128)])
+@pytest.mark.parametrize("window", [0, 45])
+@pytest.mark.parametrize("part", [0.95, -0.95])
+def test_equal_values(q4, ws, T, Hq, Hk, D, window, part):
+    """A row's rounded weights are divided by their own sum: where all values that
+    it sees are one, that is the row.  The weights are 1 (the first key that a row
+    sees, the first of all, or none) and the one whose rounding to bf16 is off by
+    0.95 of the most, all to one side; the value's last step is 2^-8 of it.  The sum
+    and the products of 9000 weights in fp32 are at most 2 9000 2^-23 apart, less
+    than half of that step."""
+    q, cache, table, lens = on_gpu(*problem([9000, 77, 8, 700], T, Hq, Hk, D, 16, 32))
+    q.zero_()[..., 0] = 1.0
+    cache[0].zero_()[..., 0] = -1.0
+    for b in range(4):
+        cache[0][table[b, 0].item(), :, 0, 0] = 0.0
+    weight = 0.75 * (1 + part * 2.0 ** -8 / 1.5)
+    cache[1].fill_(1.9921875)
+    y = q4.attention_decode(q, cache, table, lens, scale=-np.log(weight), window=window, workspace=ws)
+    assert (y == 1.9921875).all()
