@@ -987,7 +987,8 @@ def attention_decode(q, cache, table, lengths, n_new=None, scale=None, window: i
     [B] with the new tokens, n_new int32 [B] (None: T each), scale (None:
     D ** -0.5), window (0: all keys).  workspace: uint8, at least
     attention_decode_workspace_bytes, zero-filled before its first use and
-    reusable afterwards without clearing (None: one is made for the call).
+    reusable afterwards without clearing (None: one is made and cleared for the
+    call, 2 to 17 MiB, which adds 3 to 5 us to it).
     Returns bf16 [B, T, Hq, D]; rows that see no key are 0."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")

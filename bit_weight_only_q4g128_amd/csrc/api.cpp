@@ -889,6 +889,6 @@ const char* q4gemv_strerror(int status) {
     }
 }
 
-int q4gemv_version(void) { return 130; }
+int q4gemv_version(void) { return 131; }
 
 }  // extern "C"

@@ -6,11 +6,11 @@
 // those the last `window` (0: all), and of those the ones whose page is in the
 // cache.  Rows that see nothing are 0.
 //
-// Bound by memory: every key and value is read once for all heads and rows
-// that share it, 16 rows (heads of the group x new tokens) to a matrix
-// instruction, whose other rows are idle where there are fewer; the matrix
-// cores have ten times the rate that this needs, so nothing is gained by
-// filling them.
+// Bound by memory: a key and value is read once for up to 32 of the rows (heads
+// of the group x new tokens) that share it, and again for every 32 more; 16 rows
+// are a matrix instruction's, whose other rows are idle where there are fewer:
+// the matrix cores have ten times the rate that this needs, so nothing is gained
+// by filling them.
 //
 // Nothing passes through LDS on the way: a wave takes 32 keys at a time
 // straight into registers, as S^T = K Q^T and O^T = V^T P^T (16x16x32).
@@ -38,17 +38,24 @@
 // joins them, in order, so that results do not depend on timing.
 //
 // Measured (16 heads over 4, D = 128; us, and the bytes of q, y and the keys
-// and values seen at that rate):
-//   one sequence, 2304 keys, bf16                    9.3
-//   48 sequences up to 2304 keys, bf16                26   4.5 TB/s
-//   48 sequences up to 4099, 5 rows each, e4m3        36   3.0 TB/s
-//   one sequence, 131071 keys, bf16                   49   5.5 TB/s
-//   32 sequences of 32768 keys, bf16                 325   6.6 TB/s
-// the same cache again and again; another one every time (1.2 GB of them in
-// turn): 10.1, 29, 40, 64 and 347.  A copy of 2 GiB moves 4.9 TB/s, both
-// directions counted.  The last is the memory's rate; before it stand the
-// launch, the lengths, pages and heads one after the other, and behind it the
-// join, some 9 us together, which is what the first has.
+// and values seen at that rate; the same cache again and again, and another one
+// every time, 1.3 GB of them in turn):
+//   one sequence, 2304 keys, bf16                    9.9         10.5
+//   48 sequences up to 2304 keys, bf16                27   4.4    29
+//   the same, e4m3                                    20   3.0    21
+//   48 sequences up to 8192 keys, window 1024, bf16   24   4.0    26
+//   48 sequences up to 2304, 5 rows each, bf16        33   3.6    36
+//   48 sequences up to 4099, 5 rows each, e4m3        35   3.1    37
+//   4 sequences up to 8192, 64 rows each, bf16        59   0.7    59   (keys read 8 times)
+//   one sequence, 131071 keys, bf16                   49   5.5    63
+//   32 sequences of 32768 keys, bf16                 326   6.6   360
+// A copy of 2 GiB moves 4.9 TB/s, both directions counted.  The last is the
+// memory's rate; before it stand the launch, the lengths, pages and heads one
+// after the other, and behind it the join, some 9 us together, which is what
+// the first has, and half of what 48 sequences in 8 bits take.  With several
+// rows a unit's own instructions (heads, meeting, parts, joins) are half of all
+// vector instructions; among them are the 49 to 56 scalars that the compiler
+// keeps in lanes of vector registers.
 #include "attention.h"
 #include "attn_common.h"
 #include "internal.h"

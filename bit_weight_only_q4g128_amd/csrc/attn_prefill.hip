@@ -25,17 +25,21 @@
 // Each wave computes a step's weights beside the matrix instructions of both
 // products: those of this step's values, and the next step's scores.
 //
-// Measured (16 heads; us, and the products of the keys that rows see):
-//   one prompt of 77 tokens, D = 128 over 4                    7.0
-//   48 prompts up to 2304 tokens, D = 128 over 4               457    808 TFLOP/s
+// Measured (16 heads; us of a launch among others, and the products of the keys
+// that rows see; another card's are 1 to 3 % apart):
+//   one prompt of 77 tokens, D = 128 over 4                    7.7
+//   48 prompts up to 2304 tokens, D = 128 over 4               453    817 TFLOP/s
 //   5 prompts up to 1999 tokens behind 2048 keys, window
-//   1024, D = 64 over 8                                         41    578 TFLOP/s
-//   one prompt of 16384 tokens, D = 128 over 4                1008   1091 TFLOP/s
-// where the library's product of 8192 x 8192 x 8192 reaches 1605.  The long
-// prompt runs at 1.9 GHz, the board's power being what bounds it then; half the
-// heads' columns leave the exponentials half as much to hide behind; short
-// prompts pay for masked halves of the diagonal's steps and some 6000 cycles a
-// workgroup before its first product.
+//   1024, D = 64 over 8                                         39    600 TFLOP/s
+//   one prompt of 8192 tokens, D = 64 over 8                   163    842 TFLOP/s
+//   one prompt of 16384 tokens, D = 128 over 4                1017   1081 TFLOP/s
+// where the library's product of 8192 x 8192 x 8192 reaches 1605.  Neither unit
+// is full: the matrix cores are busy for 56, 40 and 23 % of the cycles of the long
+// prompt, the packed ones and the window, the vector unit for 47, 43 and 43 %, so
+// that the one hardly works while the other does.  A wave has one block of rows,
+// whose products wait for its weights; every step ends with a wait for all loads
+// and a barrier; masked steps go over their values in LDS twice more; and some
+// 6000 cycles of a workgroup pass before its first product.
 #include "attention.h"
 #include "attn_common.h"
 #include "internal.h"

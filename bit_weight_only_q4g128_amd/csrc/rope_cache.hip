@@ -20,9 +20,12 @@
 // wave's load is whole rows; the norm's sum and a group's largest value meet in
 // DPP steps, the halves of a pair by one lane move per element.
 //
-// Measured (16 heads over 4, D = 128, both norms; us): one token 3.8; 240 tokens
-// into an e4m3 cache 4.4; 16385 tokens 36.9, 5.9 TB/s of what is read and written
-// (218 MB; a copy of 2 GiB moves 4.9, both directions counted).
+// Measured (16 heads over 4, D = 128, both norms; us of a launch among others):
+// one token 4.5; 240 tokens into an e4m3 cache 5.0; 16385 tokens 37.5 into a bf16
+// cache (218 MB read and written) and 36.2 into an e4m3 one (186 MB), the same
+// again and again, of which the last level's cache holds a part; other tokens and
+// caches every time 49 and 46, 4.4 and 4.0 TB/s (a copy of 2 GiB moves 4.9, both
+// directions counted).
 #include "attention.h"
 #include "attn_common.h"
 #include "fp8_codes.h"

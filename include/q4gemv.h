@@ -566,8 +566,10 @@ typedef struct q4_kv_cache {
  * place (int64 [T]); a token whose slot is no slot of the cache (-1, say) is not
  * kept.  An e4m3 cache takes the unrounded h and v, with a the largest
  * finite |h| of the head: scale = RN(a / 448), code = RN_e4m3(h * 448 / a); a
- * value that is not finite becomes the NaN code.  Slots must differ: of a
- * slot named twice the contents are not specified (nothing else is touched).
+ * value that is not finite becomes the NaN code.  v's codes round once; k's h is
+ * an fp32 number, whose quotient rounds twice: a code whose quotient lies within
+ * 2^-24 of it of a tie of e4m3 may be the other neighbour.  Slots must differ: of
+ * a slot named twice the contents are not specified (nothing else is touched).
  *
  * 1 <= T <= 2^22, Hq and Hk 1 to 256, eps finite and > 0.  Alignment: arrays of
  * heads and norm weights 16 bytes, positions and inv_freq 4, slots 8.  No
@@ -588,7 +590,8 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * `window` (0: all).  table int32 [B, width]: page numbers, token j on page
  * table[b, j / page_size]; an entry that is no page of the cache (-1, say)
  * holds nothing, and its tokens are not seen.  Lengths are taken within
- * 0 .. width * page_size; nothing behind a sequence's length is read.
+ * 0 .. width * page_size.  Table entries behind a sequence's length are not read;
+ * keys and values behind it on its last page may be, and have no effect.
  * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
  * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
  * Keys and values that a row does not see have no effect on it, whatever they
