@@ -321,10 +321,13 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(D)) void attn_prefill_kerne
             top = max_xor32(largest(z));
         }
         // Weights may exceed 1: only a maximum that grew by more than 2^8
-        // rescales what is there, which after the first steps is rare.
-        if (__any((top - m) * p.c > 8.f)) {
-            const float now = fmaxf(m, top);
-            const float x = now == m ? 1.0f : __builtin_amdgcn_exp2f((m - now) * p.c);
+        // rescales what is there, which after the first steps is rare.  Each row
+        // goes by its own: if the others of the wave moved it along, keys that it
+        // does not see would change its roundings.
+        const bool grown = (top - m) * p.c > 8.f;
+        if (__any(grown)) {
+            const float now = grown ? top : m;
+            const float x = grown ? __builtin_amdgcn_exp2f((m - now) * p.c) : 1.0f;
             m = now;
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] *= x;

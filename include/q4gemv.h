@@ -594,8 +594,8 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * keys and values behind it on its last page may be, and have no effect.
  * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
  * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
- * Keys and values that a row does not see have no effect on it, whatever they
- * hold.  Scores, softmax and sums are fp32 (a score that leaves its range, before
+ * Keys and values that a row does not see, and other rows' queries, have no effect
+ * on it, to the last bit, whatever they hold.  Scores, softmax and sums are fp32 (a score that leaves its range, before
  * its scales or after them, is infinite); a weight (times an 8-bit value's scale)
  * is rounded to bf16 before it multiplies its value, and, where values are bf16,
  * before it is summed, so that a row is a mean of its values.

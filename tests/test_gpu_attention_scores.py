@@ -162,3 +162,28 @@ def test_scale_at_its_limits(q4, call, scale):
     for t in range(n):
         want = ve[:t + 1].mean(0)
         within(y[t, 0], want, 2.0 ** -8 * np.abs(want) + 2.0 ** -22 * (t + 1) * np.abs(ve[:t + 1]).mean(0), f"row {t}")
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("D,Hq,Hk", [(64, 2, 1), (128, 4, 2), (128, 2, 2)])
+@pytest.mark.parametrize("window", [0, 90])
+def test_rows_stand_alone(q4, call, D, Hq, Hk, window):
+    """What a row gives is its own keys' and its own query's, to the last bit:
+    neither a key that only later rows see, however large its score, nor the
+    other heads' queries beside it change it."""
+    n, g = 210, synth.make_gen(("alone", D, Hq, Hk))
+    rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k, v = rnd(n, Hq, D), rnd(n, Hk, D), rnd(n, Hk, D)
+    clean = CALLS[call](q4, q, k, v, D ** -0.5, window)
+    for j in (40, 75, 150, 170, 209):
+        loud = k.clone()
+        loud[j] *= 30
+        y = CALLS[call](q4, q, loud, v, D ** -0.5, window)
+        other = (y[:j] != clean[:j]).any(-1).any(-1)
+        assert not other.any(), f"key {j}: rows {other.nonzero()[:, 0].tolist()[:8]}"
+        assert not torch.equal(y[j:], clean[j:])
+    for h in range(Hq):
+        loud = q * 30
+        loud[:, h] = q[:, h]
+        y = CALLS[call](q4, loud, k, v, D ** -0.5, window)
+        assert torch.equal(y[:, h], clean[:, h]), f"head {h}"
