@@ -595,10 +595,11 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * q: rows b * T + i, q_stride apart; y [B, T, Hq, D] is fully overwritten: rows
  * that see no key (or only scores of -infinity), and rows behind the n-th, are 0.
  * Keys and values that a row does not see, and other rows' queries, have no effect
- * on it, to the last bit, whatever they hold.  Scores, softmax and sums are fp32 (a score that leaves its range, before
- * its scales or after them, is infinite); a weight (times an 8-bit value's scale)
- * is rounded to bf16 before it multiplies its value, and, where values are bf16,
- * before it is summed, so that a row is a mean of its values.
+ * on it, to the last bit, whatever they hold.  Scores, softmax and sums are fp32 (a
+ * score that leaves its range, before its scales or after them, is infinite); a
+ * weight (times an 8-bit value's scale) is rounded to bf16 before it multiplies
+ * its value, and, where values are bf16, before it is summed, so that a row is a
+ * mean of its values.
  *
  * 1 <= B <= 4096, 1 <= T <= 64, Hq <= 256 a multiple of Hk, width * page_size <=
  * 2^24, and B * Hk * (ceil(width * page_size / 32) + 8), times ceil(T * Hq / Hk / 32)
@@ -608,10 +609,11 @@ int q4_rope_cache(const uint16_t* q, const uint16_t* k, const uint16_t* v, int T
  * workspace: at least q4_attention_decode_workspace_bytes, 256-byte aligned,
  * zero-filled before its first use; its first 64 KiB are arrival counters that
  * every call leaves at zero, the rest is scratch, so it can be shared with the
- * library's other calls that take a workspace of this kind.  It does not depend on B or the lengths.  Calls that use one workspace
- * must not overlap in time.  Results do not depend on timing, but for one
- * sequence they may differ in their last bits with the others of its batch
- * (the work is split by the lengths of all).
+ * library's other calls that take a workspace of this kind.  It does not depend on
+ * B or the lengths.  Calls that use one workspace must not overlap in time.
+ * Results do not depend on timing, but for one sequence they may differ in their
+ * last bits with the others of its batch (the work is split by the lengths of
+ * all).
  */
 size_t q4_attention_decode_workspace_bytes(int T, int Hq, int Hk, int D);
 int q4_attention_decode(const uint16_t* q, int B, int T, int Hq, int Hk, int D, int64_t q_stride, const q4_kv_cache* cache,

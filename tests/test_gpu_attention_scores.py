@@ -187,3 +187,20 @@ def test_rows_stand_alone(q4, call, D, Hq, Hk, window):
         loud[:, h] = q[:, h]
         y = CALLS[call](q4, loud, k, v, D ** -0.5, window)
         assert torch.equal(y[:, h], clean[:, h]), f"head {h}"
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 45])
+@pytest.mark.parametrize("part", [0.95, -0.95])
+def test_equal_values(q4, call, D, window, part):
+    """A row's rounded weights are divided by their own sum: where all its values
+    are one, that is the row.  The weights are 1 (the first key's) and one whose
+    rounding to bf16 is off by 0.95 of the most, all to one side; a row's sum and its
+    products differ by less than 2 300 2^-23 of them, and the value's step is 2^-8."""
+    n = 300
+    weight = 0.75 * (1 + part * 2.0 ** -8 / 1.5)
+    k = along(np.array([[0.0]] + [[-1.0]] * (n - 1)), 1, D)
+    v = torch.full((n, 1, D), 1.9921875, dtype=torch.bfloat16, device="cuda")
+    y = CALLS[call](q4, along(np.ones((n, 2)), 2, D), k, v, -float(np.log(weight)), window)
+    assert (y == 1.9921875).all()
