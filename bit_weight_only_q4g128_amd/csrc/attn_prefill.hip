@@ -26,13 +26,13 @@
 // products: those of this step's values, and the next step's scores.
 //
 // Measured (16 heads; us of a launch among others, and the products of the keys
-// that rows see; another card's are 1 to 3 % apart):
+// that rows see; on another card up to 3 % less):
 //   one prompt of 77 tokens, D = 128 over 4                    7.7
-//   48 prompts up to 2304 tokens, D = 128 over 4               453    817 TFLOP/s
+//   48 prompts up to 2304 tokens, D = 128 over 4               468    790 TFLOP/s
 //   5 prompts up to 1999 tokens behind 2048 keys, window
-//   1024, D = 64 over 8                                         39    600 TFLOP/s
-//   one prompt of 8192 tokens, D = 64 over 8                   163    842 TFLOP/s
-//   one prompt of 16384 tokens, D = 128 over 4                1017   1081 TFLOP/s
+//   1024, D = 64 over 8                                         41    576 TFLOP/s
+//   one prompt of 8192 tokens, D = 64 over 8                   168    819 TFLOP/s
+//   one prompt of 16384 tokens, D = 128 over 4                1050   1048 TFLOP/s
 // where the library's product of 8192 x 8192 x 8192 reaches 1605.  Neither unit
 // is full: the matrix cores are busy for 56, 40 and 23 % of the cycles of the long
 // prompt, the packed ones and the window, the vector unit for 47, 43 and 43 %, so
